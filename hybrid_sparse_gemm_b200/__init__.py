@@ -8,6 +8,12 @@ module raises on import; there is no fallback.
     import hybrid_sparse_gemm_b200 as hsg
     lin = hsg.PackedLinear.pack(W, mask_bits, tile_flags, tile_rows=128, tile_cols=128)
     Y = lin(X)                       # Y = X @ (W * mask).T, bf16
+
+The same tiles in 8-bit integers, one scale per token and per output channel:
+
+    lin = hsg.PackedLinearQ8.pack(W, mask_bits, tile_flags)
+    qkv = hsg.LinearGroupQ8([q, k, v])
+    (Yq, Yk, Yv), h = qkv.norm(x, gamma, eps, residual=h)   # RMS norm -> codes -> one launch
 """
 from __future__ import annotations
 
@@ -35,7 +41,11 @@ EXPORTED = ["patch_pack", "patch_linear", "patch_linear_path", "patch_linear_hos
             "patch_info", "patch_copy_packed", "patch_check", "patch_free", "patch_last_error",
             "patch_version", "patch_plan", "patch_linear_noalloc", "patch_group_create",
             "patch_group_linear", "patch_group_path", "patch_group_free", "patch_selftest_wait",
-            "patch_partition_rows", "patch_classify_tiles", "patch_group_linear_host", "patch_plan_pairs"]
+            "patch_partition_rows", "patch_classify_tiles", "patch_group_linear_host", "patch_plan_pairs",
+            "patch_pack_q8", "patch_linear_q8", "patch_group_linear_q8", "patch_unpack_q8",
+            "patch_quantize_q8", "patch_rmsnorm_q8", "patch_silu_mul_q8", "patch_dequantize_q8"]
+TYPE_BF16, TYPE_FP16, TYPE_FP32, TYPE_INT8 = 0, 1, 2, 3
+_TYPES = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32}
 
 
 class patch_info_t(ctypes.Structure):
@@ -71,6 +81,15 @@ _lib.patch_plan.argtypes = [_I64, _I64, _P, _I, _I, _P, _P, _P, ctypes.POINTER(_
 _lib.patch_plan_pairs.argtypes = [_I64, _I64, _P, _I, _I, _P]
 _lib.patch_partition_rows.argtypes = [_I64, _I64, _P, _I, _I, _I, _I64, _P]
 _lib.patch_classify_tiles.argtypes = [_P, _I64, _I64, _I, _I, _P, ctypes.POINTER(_I64)]
+_F = ctypes.c_float
+_lib.patch_pack_q8.argtypes = [_P, _I, _P, _I64, _I64, _P, _I, _P, _I, _I, _P, ctypes.POINTER(_P)]
+_lib.patch_linear_q8.argtypes = [_P, _P, _I64, _P, _I64, _P, _I64, _I, _I, _P]
+_lib.patch_group_linear_q8.argtypes = [_P, _P, _P, _P, _I64, _P, _P, _I, _I, _P]
+_lib.patch_unpack_q8.argtypes = [_P, _P, _P, _P]
+_lib.patch_quantize_q8.argtypes = [_P, _I64, _I, _I64, _I64, _P, _I64, _P, _P]
+_lib.patch_rmsnorm_q8.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _I, _F, _I64, _I64, _P, _I64, _P, _P]
+_lib.patch_silu_mul_q8.argtypes = [_P, _I64, _P, _I64, _I, _I64, _I64, _P, _I64, _P, _P]
+_lib.patch_dequantize_q8.argtypes = [_P, _I64, _P, _I64, _I64, _P, _I64, _I, _P]
 _lib.patch_free.argtypes = [_P]
 _lib.patch_free.restype = None
 _lib.patch_last_error.restype = ctypes.c_char_p
@@ -78,7 +97,9 @@ _lib.patch_version.restype = ctypes.c_int
 for _n in ["patch_pack", "patch_linear", "patch_linear_path", "patch_linear_host", "patch_unpack",
            "patch_info", "patch_copy_packed", "patch_check", "patch_plan", "patch_linear_noalloc",
            "patch_group_create", "patch_group_linear", "patch_partition_rows", "patch_classify_tiles",
-           "patch_group_linear_host", "patch_plan_pairs"]:
+           "patch_group_linear_host", "patch_plan_pairs", "patch_pack_q8", "patch_linear_q8",
+           "patch_group_linear_q8", "patch_unpack_q8", "patch_quantize_q8", "patch_rmsnorm_q8",
+           "patch_silu_mul_q8", "patch_dequantize_q8"]:
     getattr(_lib, _n).restype = ctypes.c_int
 
 
@@ -232,6 +253,135 @@ def patch_free(h: int):
     _lib.patch_free(h)
 
 
+# ---- 8-bit integers ----------------------------------------------------------
+
+def _on_device(*tensors):
+    """Every tensor on the current CUDA device, where the calls launch."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
+
+
+def _rows(name: str, t: torch.Tensor, shape, dtype) -> int:
+    """Row pitch of a 2-D tensor of rows of contiguous elements."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    ld, step = t.stride()
+    if step != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return ld
+
+
+def _scales(name: str, t: torch.Tensor, n: int):
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{name} is {t.dtype}, not torch.float32")
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be {n} contiguous scales")
+
+
+def _row_type(x: torch.Tensor) -> int:
+    if x.dim() != 2 or x.dtype not in _TYPES:
+        raise TypeError(f"need a 2-D bf16, fp16 or fp32 tensor, not {x.dim()}-D {x.dtype}")
+    return _TYPES[x.dtype]
+
+
+def patch_pack_q8(W: torch.Tensor, mask_bits: torch.Tensor, tile_flags, tile_rows: int = 128, tile_cols: int = 128,
+                  bitorder: int = 0, w_scale: torch.Tensor | None = None, stream=None) -> int:
+    """Returns an opaque handle (int). W [N,K] on the device: bf16, quantised per
+    output channel, or int8 codes with their fp32 scales w_scale [N]."""
+    if W.dim() != 2 or not W.is_contiguous() or W.dtype not in (torch.bfloat16, torch.int8):
+        raise TypeError("W must be a contiguous 2-D bf16 or int8 tensor")
+    if mask_bits.dtype != torch.uint8 or not mask_bits.is_contiguous():
+        raise TypeError("mask_bits must be a contiguous uint8 tensor")
+    N, K = W.shape
+    if mask_bits.numel() != (N * K + 7) // 8:
+        raise ValueError(f"mask_bits has {mask_bits.numel()} bytes, a {N}x{K} mask needs {(N * K + 7) // 8}")
+    if w_scale is not None:
+        _scales("w_scale", w_scale, N)
+    _on_device(W, mask_bits, w_scale)
+    flags = torch.as_tensor(tile_flags, dtype=torch.uint8).reshape(-1).contiguous().cpu()
+    if tile_rows > 0 and tile_cols > 0 and N % tile_rows == 0 and K % tile_cols == 0 and \
+            flags.numel() != (N // tile_rows) * (K // tile_cols):
+        raise ValueError(f"tile_flags has {flags.numel()} entries, the {N}x{K} weight has "
+                         f"{(N // tile_rows) * (K // tile_cols)} tiles")
+    h = _P()
+    _check(_lib.patch_pack_q8(W.data_ptr(), TYPE_BF16 if W.dtype == torch.bfloat16 else TYPE_INT8,
+                              None if w_scale is None else w_scale.data_ptr(), N, K, mask_bits.data_ptr(), bitorder,
+                              flags.data_ptr(), tile_rows, tile_cols, _stream(stream), ctypes.byref(h)))
+    return h.value
+
+
+def patch_linear_q8(h: int, X: torch.Tensor, x_scale: torch.Tensor, Y: torch.Tensor, path: int = PATH_AUTO, stream=None):
+    """Y [M,N] (bf16, fp16 or fp32) from the codes X [M,K] and their scales [M]."""
+    _check(_lib.patch_linear_q8(h, X.data_ptr(), X.stride(0), x_scale.data_ptr(), X.shape[0], Y.data_ptr(),
+                                Y.stride(0), _TYPES[Y.dtype], path, _stream(stream)))
+
+
+def patch_unpack_q8(h: int, W: torch.Tensor, w_scale: torch.Tensor, stream=None):
+    _check(_lib.patch_unpack_q8(h, W.data_ptr(), w_scale.data_ptr(), _stream(stream)))
+
+
+def patch_quantize_q8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None):
+    """Codes q [M,K] (int8) and scales [M] (fp32) of the rows of x."""
+    t = _row_type(x)
+    _on_device(x, q, scale)
+    _scales("scale", scale, x.shape[0])
+    _check(_lib.patch_quantize_q8(x.data_ptr(), _rows("x", x, x.shape, x.dtype), t, x.shape[0], x.shape[1],
+                                  q.data_ptr(), _rows("q", q, x.shape, torch.int8), scale.data_ptr(), _stream(stream)))
+
+
+def patch_rmsnorm_q8(x: torch.Tensor, gamma: torch.Tensor, eps: float, q: torch.Tensor, scale: torch.Tensor,
+                     residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None, stream=None):
+    """Codes and scales of the RMS norm of x, or of x + residual, which is then
+    written to residual_out (which may be x or residual itself)."""
+    t = _row_type(x)
+    _on_device(x, gamma, q, scale, residual, residual_out)
+    M, K = x.shape
+    _scales("scale", scale, M)
+    if gamma.dtype is not x.dtype or gamma.shape != (K,) or (K > 1 and gamma.stride(0) != 1):
+        raise ValueError(f"gamma must be {K} contiguous elements of {x.dtype}")
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual and residual_out go together")
+    r, ldr, ro, ldo = None, 0, None, 0
+    if residual is not None:
+        r, ldr = residual.data_ptr(), _rows("residual", residual, x.shape, x.dtype)
+        ro, ldo = residual_out.data_ptr(), _rows("residual_out", residual_out, x.shape, x.dtype)
+    _check(_lib.patch_rmsnorm_q8(x.data_ptr(), _rows("x", x, x.shape, x.dtype), r, ldr, ro, ldo, gamma.data_ptr(), t,
+                                 eps, M, K, q.data_ptr(), _rows("q", q, x.shape, torch.int8), scale.data_ptr(),
+                                 _stream(stream)))
+
+
+def patch_silu_mul_q8(gate: torch.Tensor, up: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None):
+    """Codes and scales of silu(gate) * up."""
+    t = _row_type(gate)
+    _on_device(gate, up, q, scale)
+    _scales("scale", scale, gate.shape[0])
+    _check(_lib.patch_silu_mul_q8(gate.data_ptr(), _rows("gate", gate, gate.shape, gate.dtype), up.data_ptr(),
+                                  _rows("up", up, gate.shape, gate.dtype), t, gate.shape[0], gate.shape[1],
+                                  q.data_ptr(), _rows("q", q, gate.shape, torch.int8), scale.data_ptr(),
+                                  _stream(stream)))
+
+
+def patch_dequantize_q8(q: torch.Tensor, scale: torch.Tensor, out: torch.Tensor, stream=None):
+    """out = q * scale, row by row (bf16, fp16 or fp32)."""
+    t = _row_type(out)
+    _on_device(q, scale, out)
+    _scales("scale", scale, out.shape[0])
+    _check(_lib.patch_dequantize_q8(q.data_ptr(), _rows("q", q, out.shape, torch.int8), scale.data_ptr(), out.shape[0],
+                                    out.shape[1], out.data_ptr(), _rows("out", out, out.shape, out.dtype), t,
+                                    _stream(stream)))
+
+
+def _codes_like(x: torch.Tensor):
+    """Fresh (codes, scales) for the rows of x; the codes' pitch suits the products."""
+    M, K = x.shape
+    q = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=x.device)[:, :K]
+    return q, torch.empty(M, dtype=torch.float32, device=x.device)
+
+
 class LinearGroup:
     """Several packed linears run with one launch (they share M)."""
 
@@ -334,6 +484,141 @@ class PackedLinear:
     def free(self):
         if self.handle:
             patch_free(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+class PackedLinearQ8:
+    """A frozen weight packed as dense / 2:4 slabs of 8-bit codes with one scale
+    per output channel; calling it runs the layer in 8-bit integers."""
+
+    def __init__(self, handle: int, N: int, K: int):
+        self.handle = handle
+        self.N = N
+        self.K = K
+
+    @classmethod
+    def pack(cls, W, mask_bits, tile_flags, tile_rows=128, tile_cols=128, bitorder=0, w_scale=None, stream=None):
+        """W [N,K]: bf16, or int8 codes with their channel scales w_scale [N]."""
+        h = patch_pack_q8(W, mask_bits, tile_flags, tile_rows, tile_cols, bitorder, w_scale, stream)
+        return cls(h, W.shape[0], W.shape[1])
+
+    def __call__(self, X: torch.Tensor, x_scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 out_dtype: torch.dtype | None = None, path: int = PATH_AUTO, stream=None) -> torch.Tensor:
+        """X [M,K]: codes with their scales x_scale [M], or bf16 / fp16 / fp32
+        activations, which are quantised first. out_dtype: bf16 unless given (for
+        activations, their own type)."""
+        if x_scale is None:
+            x = X
+            out_dtype = out_dtype or X.dtype
+            X, x_scale = _codes_like(x)
+            patch_quantize_q8(x, X, x_scale, stream)
+        M = X.shape[0]
+        if out is None:
+            out = torch.empty((M, self.N), dtype=out_dtype or torch.bfloat16, device=X.device)
+        _rows("X", X, (M, self.K), torch.int8)
+        _rows("out", out, (M, self.N), out.dtype)
+        _scales("x_scale", x_scale, M)
+        _on_device(X, x_scale, out)
+        patch_linear_q8(self.handle, X, x_scale, out, path, stream)
+        return out
+
+    def unpack(self, stream=None):
+        """(masked codes int8 [N,K], channel scales fp32 [N])."""
+        W = torch.empty((self.N, self.K), dtype=torch.int8, device="cuda")
+        w_scale = torch.empty(self.N, dtype=torch.float32, device="cuda")
+        patch_unpack_q8(self.handle, W, w_scale, stream)
+        return W, w_scale
+
+    def info(self) -> patch_info_t:
+        return patch_info(self.handle)
+
+    def check(self, stream=None):
+        patch_check(self.handle, stream)
+
+    def free(self):
+        if self.handle:
+            patch_free(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+class LinearGroupQ8:
+    """Several 8-bit packed linears run with one launch (they share M). The
+    inputs are codes, or come from one of the operators that end in codes:
+    `quantize`, `norm` and `silu_mul` run it and then the group on its output."""
+
+    def __init__(self, linears):
+        self.linears = list(linears)
+        arr = (_P * len(self.linears))(*[l.handle for l in self.linears])
+        g = _P()
+        _check(_lib.patch_group_create(arr, len(self.linears), ctypes.byref(g)))
+        self.handle = g.value
+
+    def __call__(self, Xs, x_scales, outs=None, out_dtype: torch.dtype = torch.bfloat16, path: int = PATH_AUTO,
+                 stream=None):
+        """Xs, x_scales: one tensor of codes (and its scales) for all members, or
+        a list with one per member."""
+        n = len(self.linears)
+        if isinstance(Xs, torch.Tensor):
+            Xs, x_scales = [Xs] * n, [x_scales] * n
+        if len(Xs) != n or len(x_scales) != n or (outs is not None and len(outs) != n):
+            raise ValueError(f"the group has {n} members")
+        M = Xs[0].shape[0]
+        if outs is None:
+            outs = [torch.empty((M, l.N), dtype=out_dtype, device=Xs[0].device) for l in self.linears]
+        ldx, ldy = (_I64 * n)(), (_I64 * n)()
+        for i, l in enumerate(self.linears):
+            ldx[i] = _rows(f"X {i}", Xs[i], (M, l.K), torch.int8)
+            ldy[i] = _rows(f"out {i}", outs[i], (M, l.N), outs[0].dtype)
+            _scales(f"x_scale {i}", x_scales[i], M)
+        _on_device(*Xs, *x_scales, *outs)
+        _check(_lib.patch_group_linear_q8(self.handle, (_P * n)(*[x.data_ptr() for x in Xs]), ldx,
+                                          (_P * n)(*[x.data_ptr() for x in x_scales]), M,
+                                          (_P * n)(*[y.data_ptr() for y in outs]), ldy, _TYPES[outs[0].dtype], path,
+                                          _stream(stream)))
+        return outs
+
+    def quantize(self, x, outs=None, path: int = PATH_AUTO, stream=None):
+        """The products of the rows of x, quantised once for all members."""
+        q, scale = _codes_like(x)
+        patch_quantize_q8(x, q, scale, stream)
+        return self(q, scale, outs, x.dtype, path, stream)
+
+    def norm(self, x, gamma, eps: float, residual=None, residual_out=None, outs=None, path: int = PATH_AUTO, stream=None):
+        """(products of the RMS norm of x + residual, x + residual); without a
+        residual, (products of the norm of x, x)."""
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        q, scale = _codes_like(x)
+        patch_rmsnorm_q8(x, gamma, eps, q, scale, residual, residual_out, stream)
+        return self(q, scale, outs, x.dtype, path, stream), x if residual is None else residual_out
+
+    def silu_mul(self, gate, up, outs=None, path: int = PATH_AUTO, stream=None):
+        """The products of silu(gate) * up."""
+        q, scale = _codes_like(gate)
+        patch_silu_mul_q8(gate, up, q, scale, stream)
+        return self(q, scale, outs, gate.dtype, path, stream)
+
+    def path(self, M: int, path: int = PATH_AUTO) -> int:
+        """The explicit path a call with this M and requested path would run."""
+        out = _I()
+        _check(_lib.patch_group_path(self.handle, M, path, ctypes.byref(out)))
+        return out.value
+
+    def free(self):
+        if self.handle:
+            _lib.patch_group_free(self.handle)
             self.handle = 0
 
     def __del__(self):

@@ -18,7 +18,7 @@ FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC,-O2",
-    "--shared",
+    "--shared", "--threads", "0",
     "-Xptxas", "-v",
 ]
 

@@ -20,6 +20,7 @@
 
 #include "kernels.cuh"
 #include "patch_hybrid.h"
+#include "q8.cuh"
 
 using namespace patch;
 
@@ -103,6 +104,7 @@ patch_status prepare_device(int* dev_out, DeviceInfo* info_out) {
         PATCH_CUDA(gemm_prepare_wide(&di.wide_clusters));
         if (di.wide_clusters <= 0) di.wide_clusters = 1;
         PATCH_CUDA(decode_prepare());
+        PATCH_CUDA(q8_prepare_single());
         if (di.pair_clusters <= 0) di.pair_clusters = 1;
         it = g_dev.emplace(dev, di).first;
     }
@@ -123,6 +125,22 @@ patch_status get_encode() {
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
     if (!g_encode) return fail(PATCH_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    return PATCH_OK;
+}
+
+// 2-D int8 tensor map of activation codes: rows of `cols` codes with a pitch
+// of `pitch` bytes, 128-byte-swizzled boxes of 128 codes x box_rows.
+patch_status encode_codes(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t pitch, int box_rows) {
+    patch_status st = get_encode();
+    if (st != PATCH_OK) return st;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    cuuint32_t box[2] = {(cuuint32_t)kQ8SlabK, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PATCH_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return PATCH_OK;
 }
 
@@ -244,17 +262,21 @@ std::vector<int> pair_order(const std::vector<uint8_t>& sp, int S, int KB) {
 
 // Region V (every slab), region E (a metadata block per chunk holding a 2:4
 // slab), region D (dense images of 2:4 slabs whose partner strip is dense).
-void build_plan(Plan& p, int64_t N, int64_t K, int R, int C, const uint8_t* flags) {
+// slab_k: columns per slab, per_chunk: slabs that share a metadata block (64
+// and 2 for bf16, 128 and 1 for 8-bit codes, whose last slab may be half).
+void build_plan(Plan& p, int64_t N, int64_t K, int R, int C, const uint8_t* flags, int slab_k = kSlabK,
+                int per_chunk = 2) {
     p.S = (int)(N / kStrip);
-    p.KB = (int)(K / kSlabK);
-    p.KC = (p.KB + 1) / 2;
+    p.KB = (int)((K + slab_k - 1) / slab_k);
+    p.KC = (p.KB + per_chunk - 1) / per_chunk;
     const int64_t tiles_k = K / C;
     std::vector<uint8_t> sp((size_t)p.S * p.KB);
     for (int s = 0; s < p.S; ++s)
         for (int b = 0; b < p.KB; ++b) {
             bool all = true;
             for (int r0 = s * kStrip; r0 < (s + 1) * kStrip; r0 += R)
-                all = all && flags[(int64_t)(r0 / R) * tiles_k + ((int64_t)b * kSlabK) / C] != 0;
+                for (int64_t c0 = (int64_t)b * slab_k; c0 < std::min<int64_t>(K, (int64_t)(b + 1) * slab_k); c0 += C)
+                    all = all && flags[(int64_t)(r0 / R) * tiles_k + c0 / C] != 0;
             sp[(size_t)s * p.KB + b] = all;
         }
     auto is_sp = [&](int s, int b) { return sp[(size_t)s * p.KB + b] != 0; };
@@ -273,7 +295,7 @@ void build_plan(Plan& p, int64_t N, int64_t K, int R, int C, const uint8_t* flag
     for (int s = 0; s < p.S; ++s)
         for (int b = 0; b < p.KB; ++b) {
             const bool x = is_sp(s, b);
-            const bool first = x && (b % 2 == 0 || !is_sp(s, b - 1));
+            const bool first = x && (b % per_chunk == 0 || !is_sp(s, b - 1));
             p.slab[(size_t)s * p.KB + b] =
                 (uint32_t)((off / 16) << 2) | (first ? kSlabFirst : 0u) | (x ? kSlabSparse : 0u);
             off += x ? kSparseValBytes : kDenseSlabBytes;
@@ -283,7 +305,8 @@ void build_plan(Plan& p, int64_t N, int64_t K, int R, int C, const uint8_t* flag
         }
     for (int s = 0; s < p.S; ++s)
         for (int c = 0; c < p.KC; ++c) {
-            bool any = is_sp(s, 2 * c) || (2 * c + 1 < p.KB && is_sp(s, 2 * c + 1));
+            bool any = false;
+            for (int b = c * per_chunk; b < std::min(p.KB, (c + 1) * per_chunk); ++b) any = any || is_sp(s, b);
             if (any) {
                 p.meta[(size_t)s * p.KC + c] = (uint32_t)(off / 16);
                 off += kMetaBytes;
@@ -302,7 +325,7 @@ void build_plan(Plan& p, int64_t N, int64_t K, int R, int C, const uint8_t* flag
             } else {
                 a_off = (int64_t)slab_offset_bytes(p.slab[(size_t)s * p.KB + b]);
             }
-            const bool first = px && (b % 2 == 0 || !pair_sp(s, b - 1));
+            const bool first = px && (b % per_chunk == 0 || !pair_sp(s, b - 1));
             p.gemm[(size_t)s * p.KB + b] =
                 (uint32_t)((a_off / 16) << 2) | (first ? kSlabFirst : 0u) | (px ? kSlabSparse : 0u);
             p.pair_sparse += px;
@@ -350,6 +373,8 @@ struct patch_handle_s {
     DeviceInfo dev;
     int64_t N = 0, K = 0;
     int R = 0, C = 0;
+    bool q8 = false;            // 8-bit codes (patch_pack_q8), else bf16
+    float* w_scale = nullptr;   // N channel scales of a q8 handle
     Plan plan;
     uint8_t* packed = nullptr;
     uint32_t* slab_dev = nullptr;
@@ -377,6 +402,7 @@ struct patch_group_s {
     int device = 0;
     DeviceInfo dev;
     int n = 0;
+    bool q8 = false;              // every member holds 8-bit codes
     patch_handle h[kMaxGroup] = {};
     int parts[kMaxGroup] = {};    // decode K-parts per strip of each member in this group
     int parts_w[kMaxGroup] = {};  // the same for the decode kernel's 64-token instance
@@ -469,6 +495,7 @@ void free_handle(patch_handle h) {
     cudaDeviceSynchronize();
     free_group(h->self);
     cudaFree(h->packed);
+    cudaFree(h->w_scale);
     cudaFree(h->slab_dev);
     cudaFree(h->order_dev);
     cudaFree(h->pgemm_dev);
@@ -487,6 +514,7 @@ patch_status make_group(const patch_handle* hs, int n, patch_group* out) {
     g->device = hs[0]->device;
     g->dev = hs[0]->dev;
     g->n = n;
+    g->q8 = hs[0]->q8;
     g->status_dev = hs[0]->status_dev;
     g->pure24 = true;
     for (int i = 0; i < n; ++i)
@@ -622,7 +650,12 @@ patch_status get_decode_ws(patch_group g, cudaStream_t st, int bn, const DecodeW
 // MMAs, 4 CTA pair with two strips per CTA, 5 decode with 64-token MMAs):
 // tokens per tile,
 // activation rows per TMA box, weight rows of a work unit, persistent slots.
+// 8-bit kernels: 10 + the number of their bf16 counterpart.
+constexpr int kQ8Kernel = 10;
+constexpr int64_t kQ8MaxK = 131008;  // K * 128 * 128 stays below 2^31
+
 int kernel_bn(int kernel) {
+    kernel %= kQ8Kernel;
     return kernel == 0   ? kGemmBN
            : kernel == 2 ? kDecodeBN
            : kernel == 5 ? kDecodeWideBN
@@ -633,10 +666,12 @@ int kernel_box_rows(int kernel) {
     return kernel == 1 ? kGemm2BN / 2 : kernel == 4 ? kGemm22BN / 2 : kernel_bn(kernel);
 }
 int64_t kernel_rows(const Plan& p, int kernel) {
+    kernel %= kQ8Kernel;
     const int64_t pairs = (int64_t)p.pair_cost.size();
     return kernel == 0 ? (int64_t)p.strip_cost.size() : kernel == 1 ? pairs : (pairs + 1) / 2;
 }
 int kernel_slots(const DeviceInfo& d, int kernel) {
+    kernel %= kQ8Kernel;
     return kernel == 1   ? d.pair_clusters
            : kernel == 4 ? d.wide_clusters
            : kernel == 2 ? kDecodeCtasPerSm * d.sms
@@ -650,6 +685,8 @@ void lpt_schedule(patch_group g, int kernel, int mb, std::vector<int>& off, std:
         int id;
     };
     std::vector<Unit> units;
+    const int slots = kernel_slots(g->dev, kernel);
+    kernel %= kQ8Kernel;
     for (int l = 0; l < g->n; ++l) {
         const Plan& p = g->h[l]->plan;
         if (kernel == 0 || kernel == 1) {
@@ -671,7 +708,7 @@ void lpt_schedule(patch_group g, int kernel, int mb, std::vector<int>& off, std:
         }
     }
     std::stable_sort(units.begin(), units.end(), [](const Unit& x, const Unit& y) { return x.cost > y.cost; });
-    const int grid = std::max(1, std::min(kernel_slots(g->dev, kernel), (int)units.size()));
+    const int grid = std::max(1, std::min(slots, (int)units.size()));
     using Item = std::pair<double, int>;
     std::priority_queue<Item, std::vector<Item>, std::greater<Item>> pq;
     for (int c = 0; c < grid; ++c) pq.push({0.0, c});
@@ -900,6 +937,122 @@ patch_status run_group(patch_group g, const void* const* X, int64_t M, void* con
     return PATCH_OK;
 }
 
+// The kernel an 8-bit call runs. GEMM_SINGLE: any M.
+patch_status resolve_path_q8(patch_group g, int path, int64_t M, int* out) {
+    (void)g;
+    (void)M;
+    if (path == PATCH_PATH_AUTO || path == PATCH_PATH_GEMM) path = PATCH_PATH_GEMM_SINGLE;
+    if (path != PATCH_PATH_GEMM_SINGLE) return fail(PATCH_ERR_UNSUPPORTED, "path %d has no 8-bit kernel", path);
+    *out = path;
+    return PATCH_OK;
+}
+
+// One launch over every member of an 8-bit group.
+patch_status run_group_q8(patch_group g, const int8_t* const* X, const int64_t* ldx, const float* const* x_scale,
+                          int64_t M, void* const* Y, const int64_t* ldy, int y_type, int path, cudaStream_t st) {
+    patch_status s = resolve_path_q8(g, path, M, &path);
+    if (s != PATCH_OK) return s;
+    const int kernel = kQ8Kernel;
+    const int bn = kernel_bn(kernel);
+    const int mb = (int)((M + bn - 1) / bn);
+    const int n_tok = (int)std::min<int64_t>(bn, (M + 15) & ~(int64_t)15);  // tokens per MMA and per activation box
+    GroupMaps maps;
+    Q8Args a;
+    memset(&maps, 0, sizeof(maps));
+    memset(&a, 0, sizeof(a));
+    for (int l = 0; l < g->n; ++l) {
+        patch_handle h = g->h[l];
+        if (kernel_rows(h->plan, kernel) * mb > kUnitMask)
+            return fail(PATCH_ERR_SHAPE, "M=%lld gives more than %d output tiles", (long long)M, kUnitMask);
+        // a single row needs no pitch, but the map wants a multiple of 16 bytes
+        const int64_t pitch = M == 1 ? (h->K + 15) & ~(int64_t)15 : ldx ? ldx[l] : h->K;
+        if ((s = encode_codes(&maps.x[l], X[l], h->K, M, pitch, n_tok)) != PATCH_OK) return s;
+        maps.a32[l] = h->tm_a32;
+        maps.a16[l] = h->tm_a16;
+        maps.a8[l] = h->tm_a8;
+        maps.e[l] = h->tm_e;
+        a.Y[l] = Y[l];
+        a.ldy[l] = ldy ? ldy[l] : h->N;
+        a.x_scale[l] = x_scale[l];
+        a.w_scale[l] = h->w_scale;
+    }
+    WorkList* wl = nullptr;
+    if ((s = get_worklist(g, kernel, mb, st, &wl)) != PATCH_OK) return s;
+    a.lins = g->lins_dev;
+    a.work_off = wl->off;
+    a.work = wl->work;
+    a.M = (int)M;
+    a.MB = mb;
+    a.status = g->status_dev;
+    cudaError_t e = launch_q8_gemm(maps, a, y_type, n_tok, wl->grid, st);
+    if (e != cudaSuccess) return cuda_fail(e, "8-bit kernel launch");
+    return PATCH_OK;
+}
+
+int64_t type_size(int type) { return type == PATCH_FP32 ? 4 : type == PATCH_INT8 ? 1 : 2; }
+
+// The operands of one member of an 8-bit product.
+patch_status check_q8(patch_handle h, const int8_t* X, int64_t ldx, const float* x_scale, int64_t M, void* Y,
+                      int64_t ldy, int y_type) {
+    if (!X || !x_scale || !Y) return fail(PATCH_ERR_ARG, "X, x_scale and Y must be non-NULL");
+    if (!aligned16(X) || !aligned16(Y)) return fail(PATCH_ERR_ALIGN, "X and Y must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(x_scale) & 3u) return fail(PATCH_ERR_ALIGN, "x_scale must be 4-byte aligned");
+    if (M == 1) return PATCH_OK;
+    if (ldx < h->K || ldy < h->N)
+        return fail(PATCH_ERR_SHAPE, "row pitch below the row's length (X %lld < %lld or Y %lld < %lld)", (long long)ldx,
+                    (long long)h->K, (long long)ldy, (long long)h->N);
+    if (ldx % 16 || (ldy * type_size(y_type)) % 16)
+        return fail(PATCH_ERR_ALIGN, "row pitches must be multiples of 16 bytes");
+    if (ldx > ((int64_t)1 << 40) - 16) return fail(PATCH_ERR_SHAPE, "row pitch of X too large");
+    return PATCH_OK;
+}
+
+patch_status check_q8_call(bool q8, int64_t M, int y_type, int path) {
+    if (!q8) return fail(PATCH_ERR_ARG, "the weights are bf16: use the call without _q8");
+    if (M < 0) return fail(PATCH_ERR_ARG, "M must be >= 0");
+    if (y_type != PATCH_BF16 && y_type != PATCH_FP16 && y_type != PATCH_FP32)
+        return fail(PATCH_ERR_ARG, "y_type must be PATCH_BF16, PATCH_FP16 or PATCH_FP32 (got %d)", y_type);
+    if (path < PATCH_PATH_AUTO || path > PATCH_PATH_GEMM_WIDE_24) return fail(PATCH_ERR_ARG, "unknown path %d", path);
+    if (M > (int64_t)INT32_MAX / 2) return fail(PATCH_ERR_SHAPE, "M too large");
+    return PATCH_OK;
+}
+
+// One matrix of a row operator: rows of K elements with a pitch.
+patch_status check_rows(const char* name, const void* p, int64_t ld, int64_t M, int64_t K, int type) {
+    if (!p) return fail(PATCH_ERR_ARG, "%s must be non-NULL", name);
+    if (reinterpret_cast<uintptr_t>(p) % type_size(type))
+        return fail(PATCH_ERR_ALIGN, "%s is not aligned to its elements", name);
+    if (M > 1 && ld < K)
+        return fail(PATCH_ERR_SHAPE, "%s: row pitch %lld below K = %lld", name, (long long)ld, (long long)K);
+    return PATCH_OK;
+}
+
+patch_status check_row_sizes(int64_t M, int64_t K, int type) {
+    if (type != PATCH_BF16 && type != PATCH_FP16 && type != PATCH_FP32)
+        return fail(PATCH_ERR_ARG, "type must be PATCH_BF16, PATCH_FP16 or PATCH_FP32 (got %d)", type);
+    if (M < 0) return fail(PATCH_ERR_ARG, "M must be >= 0");
+    if (K < 1) return fail(PATCH_ERR_SHAPE, "K must be positive");
+    if (M > INT32_MAX || K > (1 << 24)) return fail(PATCH_ERR_SHAPE, "M or K too large");
+    return PATCH_OK;
+}
+
+// Launch of a row operator; a.ld* are ignored by a single row, whose tests
+// for wide accesses should then not depend on them.
+patch_status run_rows(RowArgs a, int mode, int type, void* stream) {
+    if (a.M == 1) a.ldx = a.ldr = a.ldo = a.ldq = 0;
+    int dev = 0, sms = 0;
+    PATCH_CUDA(cudaGetDevice(&dev));
+    PATCH_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    cudaError_t e = launch_rows_q8(a, mode, type, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "row kernel launch");
+    return PATCH_OK;
+}
+
+patch_status check_bf16(bool q8) {
+    if (q8) return fail(PATCH_ERR_ARG, "the weights are 8-bit codes: use the _q8 call");
+    return PATCH_OK;
+}
+
 patch_status check_xy(const void* X, const void* Y) {
     if (!X || !Y) return fail(PATCH_ERR_ARG, "X and Y must be non-NULL");
     if (!aligned16(X) || !aligned16(Y)) return fail(PATCH_ERR_ALIGN, "X and Y must be 16-byte aligned");
@@ -1033,11 +1186,15 @@ patch_status patch_partition_rows(int64_t N, int64_t K, const uint8_t* tile_flag
     return PATCH_OK;
 }
 
-patch_status patch_pack(const void* W_bf16, int64_t N, int64_t K, const uint8_t* mask_bits, int bitorder,
-                        const uint8_t* tile_flags, int tile_rows, int tile_cols, void* stream,
-                        patch_handle* out) {
-    if (!out) return fail(PATCH_ERR_ARG, "out is NULL");
-    *out = nullptr;
+}  // extern "C"
+
+namespace {
+
+// patch_pack, and patch_pack_q8 (q8 set; W is then bf16, or int8 codes with
+// their channel scales).
+patch_status pack_weights(const void* W_bf16, bool q8, const float* w_scale, int64_t N, int64_t K,
+                          const uint8_t* mask_bits, int bitorder, const uint8_t* tile_flags, int tile_rows,
+                          int tile_cols, void* stream, patch_handle* out) {
     if (!W_bf16 || !mask_bits || !tile_flags)
         return fail(PATCH_ERR_ARG, "W, mask_bits and tile_flags must be non-NULL");
     if (bitorder != 0 && bitorder != 1) return fail(PATCH_ERR_ARG, "bitorder must be 0 or 1");
@@ -1061,7 +1218,8 @@ patch_status patch_pack(const void* W_bf16, int64_t N, int64_t K, const uint8_t*
     h->K = K;
     h->R = tile_rows;
     h->C = tile_cols;
-    build_plan(h->plan, N, K, tile_rows, tile_cols, tile_flags);
+    h->q8 = q8;
+    build_plan(h->plan, N, K, tile_rows, tile_cols, tile_flags, q8 ? kQ8SlabK : kSlabK, q8 ? 1 : 2);
     const Plan& p = h->plan;
     if (p.bytes / 16 >= ((int64_t)1 << 30)) {
         free_handle(h);
@@ -1088,7 +1246,8 @@ patch_status patch_pack(const void* W_bf16, int64_t N, int64_t K, const uint8_t*
         cudaMalloc(&h->gemm_dev, sizeof(uint32_t) * p.gemm.size()) != cudaSuccess ||
         cudaMalloc(&h->status_dev, sizeof(int)) != cudaSuccess ||
         cudaMalloc(&flags_dev, ntiles) != cudaSuccess ||
-        cudaMalloc(&counters, 3 * sizeof(unsigned long long)) != cudaSuccess) {
+        (q8 && cudaMalloc(&h->w_scale, sizeof(float) * N) != cudaSuccess) ||
+        cudaMalloc(&counters, 4 * sizeof(unsigned long long)) != cudaSuccess) {
         cudaGetLastError();
         return cleanup(fail(PATCH_ERR_NOMEM, "device allocation of %lld packed bytes failed", (long long)p.bytes));
     }
@@ -1115,32 +1274,56 @@ patch_status patch_pack(const void* W_bf16, int64_t N, int64_t K, const uint8_t*
         (e = cudaMemcpyAsync(h->pmeta_dev, p.pmeta.data(), sizeof(uint32_t) * p.pmeta.size(),
                              cudaMemcpyHostToDevice, s)) != cudaSuccess ||
         (e = cudaMemcpyAsync(flags_dev, tile_flags, ntiles, cudaMemcpyHostToDevice, s)) != cudaSuccess ||
-        (e = cudaMemsetAsync(counters, 0, 3 * sizeof(unsigned long long), s)) != cudaSuccess ||
+        (e = cudaMemsetAsync(counters, 0, 4 * sizeof(unsigned long long), s)) != cudaSuccess ||
+        (w_scale && (e = cudaMemcpyAsync(h->w_scale, w_scale, sizeof(float) * N, cudaMemcpyDeviceToDevice, s)) !=
+                        cudaSuccess) ||
         (e = cudaMemsetAsync(h->status_dev, 0, sizeof(int), s)) != cudaSuccess)
         return cleanup(cuda_fail(e, "pack set-up copies"));
-    PackArgs a;
-    a.W = static_cast<const uint16_t*>(W_bf16);
-    a.bits = mask_bits;
-    a.bitorder = bitorder;
-    a.flags = flags_dev;
-    a.slab = h->slab_dev;
-    a.meta = h->meta_dev;
-    a.gemm = h->gemm_dev;
-    a.out = h->packed;
-    a.K = K;
-    a.R = tile_rows;
-    a.C = tile_cols;
-    a.KB = p.KB;
-    a.KC = p.KC;
-    a.counters = counters;
-    pack_kernel<<<p.S * p.KB, 256, 0, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cleanup(cuda_fail(e, "pack kernel launch"));
-    unsigned long long cnt[3] = {0, 0, 0};
+    if (q8) {
+        Q8PackArgs a;
+        a.W = W_bf16;
+        a.w_int8 = w_scale != nullptr;
+        a.bits = mask_bits;
+        a.bitorder = bitorder;
+        a.flags = flags_dev;
+        a.slab = h->slab_dev;
+        a.meta = h->meta_dev;
+        a.gemm = h->gemm_dev;
+        a.w_scale = h->w_scale;
+        a.out = h->packed;
+        a.K = K;
+        a.R = tile_rows;
+        a.C = tile_cols;
+        a.KB = p.KB;
+        a.counters = counters;
+        if ((e = launch_q8_pack(a, p.S, s)) != cudaSuccess) return cleanup(cuda_fail(e, "pack kernel launch"));
+    } else {
+        PackArgs a;
+        a.W = static_cast<const uint16_t*>(W_bf16);
+        a.bits = mask_bits;
+        a.bitorder = bitorder;
+        a.flags = flags_dev;
+        a.slab = h->slab_dev;
+        a.meta = h->meta_dev;
+        a.gemm = h->gemm_dev;
+        a.out = h->packed;
+        a.K = K;
+        a.R = tile_rows;
+        a.C = tile_cols;
+        a.KB = p.KB;
+        a.KC = p.KC;
+        a.counters = counters;
+        pack_kernel<<<p.S * p.KB, 256, 0, s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return cleanup(cuda_fail(e, "pack kernel launch"));
+    }
+    unsigned long long cnt[4] = {0, 0, 0, 0};
     if ((e = cudaMemcpyAsync(cnt, counters, sizeof(cnt), cudaMemcpyDeviceToHost, s)) != cudaSuccess ||
         (e = cudaStreamSynchronize(s)) != cudaSuccess)
         return cleanup(cuda_fail(e, "pack kernel"));
     if (cnt[0] != 0)
         return cleanup(fail(PATCH_ERR_MASK, "%llu groups inside 2:4 tiles do not keep exactly two of four", cnt[0]));
+    if (cnt[3] != 0)
+        return cleanup(fail(PATCH_ERR_ARG, "%llu output channels keep a NaN or an infinity", cnt[3]));
     h->desc.packed = h->packed;
     h->desc.slab = h->slab_dev;
     h->desc.meta = h->meta_dev;
@@ -1175,14 +1358,44 @@ patch_status patch_pack(const void* W_bf16, int64_t N, int64_t K, const uint8_t*
     return cleanup(PATCH_OK);
 }
 
+}  // namespace
+
+extern "C" {
+
+patch_status patch_pack(const void* W_bf16, int64_t N, int64_t K, const uint8_t* mask_bits, int bitorder,
+                        const uint8_t* tile_flags, int tile_rows, int tile_cols, void* stream,
+                        patch_handle* out) {
+    if (!out) return fail(PATCH_ERR_ARG, "out is NULL");
+    *out = nullptr;
+    return pack_weights(W_bf16, false, nullptr, N, K, mask_bits, bitorder, tile_flags, tile_rows, tile_cols, stream,
+                        out);
+}
+
+patch_status patch_pack_q8(const void* W, int w_type, const float* w_scale, int64_t N, int64_t K,
+                           const uint8_t* mask_bits, int bitorder, const uint8_t* tile_flags, int tile_rows,
+                           int tile_cols, void* stream, patch_handle* out) {
+    if (!out) return fail(PATCH_ERR_ARG, "out is NULL");
+    *out = nullptr;
+    if (w_type != PATCH_BF16 && w_type != PATCH_INT8)
+        return fail(PATCH_ERR_ARG, "w_type must be PATCH_BF16 or PATCH_INT8 (got %d)", w_type);
+    if ((w_scale != nullptr) != (w_type == PATCH_INT8))
+        return fail(PATCH_ERR_ARG, "w_scale goes with int8 codes, and only with them");
+    if (w_scale && (reinterpret_cast<uintptr_t>(w_scale) & 3u))
+        return fail(PATCH_ERR_ALIGN, "w_scale must be 4-byte aligned");
+    if (K > kQ8MaxK)
+        return fail(PATCH_ERR_SHAPE, "8-bit weights take K <= %lld, which keeps the int32 sums exact", (long long)kQ8MaxK);
+    return pack_weights(W, true, w_scale, N, K, mask_bits, bitorder, tile_flags, tile_rows, tile_cols, stream, out);
+}
+
 patch_status patch_linear_path(patch_handle h, const void* X_bf16, int64_t M, void* Y_bf16, int path,
                                void* stream) {
     if (!h) return fail(PATCH_ERR_ARG, "handle is NULL");
     if (M < 0) return fail(PATCH_ERR_ARG, "M must be >= 0");
     if (path < PATCH_PATH_AUTO || path > PATCH_PATH_GEMM_WIDE_24) return fail(PATCH_ERR_ARG, "unknown path %d", path);
-    if (M == 0) return PATCH_OK;
-    patch_status st = check_xy(X_bf16, Y_bf16);
+    patch_status st = check_bf16(h->q8);
     if (st != PATCH_OK) return st;
+    if (M == 0) return PATCH_OK;
+    if ((st = check_xy(X_bf16, Y_bf16)) != PATCH_OK) return st;
     if ((st = check_device_is(h->device)) != PATCH_OK) return st;
     const void* xs[1] = {X_bf16};
     void* ys[1] = {Y_bf16};
@@ -1196,10 +1409,11 @@ patch_status patch_linear(patch_handle h, const void* X_bf16, int64_t M, void* Y
 patch_status patch_linear_host(patch_handle h, const void* X_host, int64_t M, void* Y_host, void* stream) {
     if (!h) return fail(PATCH_ERR_ARG, "handle is NULL");
     if (M < 0) return fail(PATCH_ERR_ARG, "M must be >= 0");
+    patch_status st = check_bf16(h->q8);
+    if (st != PATCH_OK) return st;
     if (M == 0) return PATCH_OK;
     if (!X_host || !Y_host) return fail(PATCH_ERR_ARG, "X and Y must be non-NULL");
-    patch_status st = check_device_is(h->device);
-    if (st != PATCH_OK) return st;
+    if ((st = check_device_is(h->device)) != PATCH_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     std::lock_guard<std::mutex> lk(h->mu);
     const size_t xb = (size_t)M * h->K * 2, yb = (size_t)M * h->N * 2;
@@ -1240,6 +1454,7 @@ patch_status patch_group_create(const patch_handle* handles, int n, patch_group*
     for (int i = 0; i < n; ++i) {
         if (!handles[i]) return fail(PATCH_ERR_ARG, "handle %d is NULL", i);
         if (handles[i]->device != handles[0]->device) return fail(PATCH_ERR_ARG, "handles live on different devices");
+        if (handles[i]->q8 != handles[0]->q8) return fail(PATCH_ERR_ARG, "bf16 and 8-bit handles cannot share a group");
     }
     patch_status st = check_device_is(handles[0]->device);
     if (st != PATCH_OK) return st;
@@ -1252,13 +1467,12 @@ patch_status patch_group_linear(patch_group g, const void* const* X, int64_t M, 
     if (!X || !Y) return fail(PATCH_ERR_ARG, "X and Y arrays must be non-NULL");
     if (M < 0) return fail(PATCH_ERR_ARG, "M must be >= 0");
     if (path < PATCH_PATH_AUTO || path > PATCH_PATH_GEMM_WIDE_24) return fail(PATCH_ERR_ARG, "unknown path %d", path);
-    if (M == 0) return PATCH_OK;
-    for (int l = 0; l < g->n; ++l) {
-        patch_status st = check_xy(X[l], Y[l]);
-        if (st != PATCH_OK) return st;
-    }
-    patch_status st = check_device_is(g->device);
+    patch_status st = check_bf16(g->q8);
     if (st != PATCH_OK) return st;
+    if (M == 0) return PATCH_OK;
+    for (int l = 0; l < g->n; ++l)
+        if ((st = check_xy(X[l], Y[l])) != PATCH_OK) return st;
+    if ((st = check_device_is(g->device)) != PATCH_OK) return st;
     return run_group(g, X, M, Y, path, static_cast<cudaStream_t>(stream));
 }
 
@@ -1266,6 +1480,7 @@ patch_status patch_group_path(patch_group g, int64_t M, int path, int* out) {
     if (!g || !out) return fail(PATCH_ERR_ARG, "group and out must be non-NULL");
     if (M < 0) return fail(PATCH_ERR_ARG, "M must be >= 0");
     if (path < PATCH_PATH_AUTO || path > PATCH_PATH_GEMM_WIDE_24) return fail(PATCH_ERR_ARG, "unknown path %d", path);
+    if (g->q8) return resolve_path_q8(g, path, M, out);
     *out = resolve_path(g, path, M);
     return PATCH_OK;
 }
@@ -1278,12 +1493,13 @@ patch_status patch_group_linear_host(patch_group g, const void* const* X_host, i
     if (!X_host || !Y_host) return fail(PATCH_ERR_ARG, "X and Y arrays must be non-NULL");
     if (M < 0) return fail(PATCH_ERR_ARG, "M must be >= 0");
     if (path < PATCH_PATH_AUTO || path > PATCH_PATH_GEMM_WIDE_24) return fail(PATCH_ERR_ARG, "unknown path %d", path);
+    patch_status st = check_bf16(g->q8);
+    if (st != PATCH_OK) return st;
     for (int l = 0; l < g->n; ++l)
         if (!X_host[l] || !Y_host[l]) return fail(PATCH_ERR_ARG, "member %d: X and Y must be non-NULL", l);
     if (M == 0) return PATCH_OK;
     if (M > (int64_t)INT32_MAX / 2) return fail(PATCH_ERR_SHAPE, "M too large");
-    patch_status st = check_device_is(g->device);
-    if (st != PATCH_OK) return st;
+    if ((st = check_device_is(g->device)) != PATCH_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     std::lock_guard<std::mutex> lk(g->host_mu);
 
@@ -1405,8 +1621,9 @@ patch_status patch_selftest_wait(void* stream) {
 patch_status patch_unpack(patch_handle h, void* W_masked_bf16, void* stream) {
     if (!h || !W_masked_bf16) return fail(PATCH_ERR_ARG, "handle and output must be non-NULL");
     if (!aligned16(W_masked_bf16)) return fail(PATCH_ERR_ALIGN, "output must be 16-byte aligned");
-    patch_status st = check_device_is(h->device);
+    patch_status st = check_bf16(h->q8);
     if (st != PATCH_OK) return st;
+    if ((st = check_device_is(h->device)) != PATCH_OK) return st;
     unpack_kernel<<<h->plan.S * h->plan.KB, 256, 0, static_cast<cudaStream_t>(stream)>>>(
         h->packed, h->slab_dev, h->meta_dev, h->plan.KB, h->plan.KC, h->K, static_cast<uint16_t*>(W_masked_bf16));
     PATCH_CUDA(cudaGetLastError());
@@ -1466,6 +1683,137 @@ patch_status patch_check(patch_handle h, void* stream) {
 
 void patch_free(patch_handle h) { free_handle(h); }
 
+// ---- 8-bit integer path ------------------------------------------------------
+
+patch_status patch_linear_q8(patch_handle h, const int8_t* X, int64_t ldx, const float* x_scale, int64_t M, void* Y,
+                             int64_t ldy, int y_type, int path, void* stream) {
+    if (!h) return fail(PATCH_ERR_ARG, "handle is NULL");
+    patch_status st = check_q8_call(h->q8, M, y_type, path);
+    if (st != PATCH_OK) return st;
+    if (M == 0) return PATCH_OK;
+    if ((st = check_q8(h, X, ldx, x_scale, M, Y, ldy, y_type)) != PATCH_OK) return st;
+    if ((st = check_device_is(h->device)) != PATCH_OK) return st;
+    return run_group_q8(h->self, &X, &ldx, &x_scale, M, &Y, &ldy, y_type, path, static_cast<cudaStream_t>(stream));
+}
+
+patch_status patch_group_linear_q8(patch_group g, const int8_t* const* X, const int64_t* ldx,
+                                   const float* const* x_scale, int64_t M, void* const* Y, const int64_t* ldy,
+                                   int y_type, int path, void* stream) {
+    if (!g) return fail(PATCH_ERR_ARG, "group is NULL");
+    if (!X || !x_scale || !Y) return fail(PATCH_ERR_ARG, "X, x_scale and Y arrays must be non-NULL");
+    patch_status st = check_q8_call(g->q8, M, y_type, path);
+    if (st != PATCH_OK) return st;
+    if (M == 0) return PATCH_OK;
+    for (int l = 0; l < g->n; ++l) {
+        patch_handle h = g->h[l];
+        if ((st = check_q8(h, X[l], ldx ? ldx[l] : h->K, x_scale[l], M, Y[l], ldy ? ldy[l] : h->N, y_type)) != PATCH_OK)
+            return st;
+    }
+    if ((st = check_device_is(g->device)) != PATCH_OK) return st;
+    return run_group_q8(g, X, ldx, x_scale, M, Y, ldy, y_type, path, static_cast<cudaStream_t>(stream));
+}
+
+patch_status patch_unpack_q8(patch_handle h, int8_t* W, float* w_scale, void* stream) {
+    if (!h || !W || !w_scale) return fail(PATCH_ERR_ARG, "handle and outputs must be non-NULL");
+    if (!h->q8) return fail(PATCH_ERR_ARG, "the weights are bf16: use the call without _q8");
+    if (!aligned16(W)) return fail(PATCH_ERR_ALIGN, "output must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(w_scale) & 3u) return fail(PATCH_ERR_ALIGN, "w_scale must be 4-byte aligned");
+    patch_status st = check_device_is(h->device);
+    if (st != PATCH_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    PATCH_CUDA(launch_q8_unpack(h->packed, h->slab_dev, h->meta_dev, h->plan.S, h->plan.KB, h->K, W, s));
+    PATCH_CUDA(cudaMemcpyAsync(w_scale, h->w_scale, sizeof(float) * h->N, cudaMemcpyDeviceToDevice, s));
+    return PATCH_OK;
+}
+
+patch_status patch_quantize_q8(const void* x, int64_t ldx, int type, int64_t M, int64_t K, int8_t* q, int64_t ldq,
+                               float* scale, void* stream) {
+    patch_status st = check_row_sizes(M, K, type);
+    if (st != PATCH_OK || M == 0) return st;
+    if ((st = check_rows("x", x, ldx, M, K, type)) != PATCH_OK ||
+        (st = check_rows("q", q, ldq, M, K, PATCH_INT8)) != PATCH_OK ||
+        (st = check_rows("scale", scale, 1, 1, 1, PATCH_FP32)) != PATCH_OK)
+        return st;
+    RowArgs a = {};
+    a.x = x;
+    a.ldx = ldx;
+    a.M = M;
+    a.K = (int)K;
+    a.q = q;
+    a.ldq = ldq;
+    a.scale = scale;
+    return run_rows(a, kRowQuantize, type, stream);
+}
+
+patch_status patch_rmsnorm_q8(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* residual_out,
+                              int64_t ldo, const void* gamma, int type, float eps, int64_t M, int64_t K, int8_t* q,
+                              int64_t ldq, float* scale, void* stream) {
+    patch_status st = check_row_sizes(M, K, type);
+    if (st != PATCH_OK) return st;
+    if (!(eps >= 0.f) || std::isinf(eps)) return fail(PATCH_ERR_ARG, "eps must be finite and not negative");
+    if ((residual != nullptr) != (residual_out != nullptr))
+        return fail(PATCH_ERR_ARG, "residual and residual_out go together");
+    if (M == 0) return PATCH_OK;
+    if ((st = check_rows("x", x, ldx, M, K, type)) != PATCH_OK ||
+        (residual && (st = check_rows("residual", residual, ldr, M, K, type)) != PATCH_OK) ||
+        (residual && (st = check_rows("residual_out", residual_out, ldo, M, K, type)) != PATCH_OK) ||
+        (st = check_rows("gamma", gamma, K, 1, K, type)) != PATCH_OK ||
+        (st = check_rows("q", q, ldq, M, K, PATCH_INT8)) != PATCH_OK ||
+        (st = check_rows("scale", scale, 1, 1, 1, PATCH_FP32)) != PATCH_OK)
+        return st;
+    RowArgs a = {};
+    a.x = x;
+    a.ldx = ldx;
+    a.r = residual;
+    a.ldr = ldr;
+    a.ro = residual_out;
+    a.ldo = ldo;
+    a.gamma = gamma;
+    a.eps = eps;
+    a.M = M;
+    a.K = (int)K;
+    a.q = q;
+    a.ldq = ldq;
+    a.scale = scale;
+    return run_rows(a, residual ? kRowNormResidual : kRowNorm, type, stream);
+}
+
+patch_status patch_silu_mul_q8(const void* gate, int64_t ldg, const void* up, int64_t ldu, int type, int64_t M,
+                               int64_t K, int8_t* q, int64_t ldq, float* scale, void* stream) {
+    patch_status st = check_row_sizes(M, K, type);
+    if (st != PATCH_OK || M == 0) return st;
+    if ((st = check_rows("gate", gate, ldg, M, K, type)) != PATCH_OK ||
+        (st = check_rows("up", up, ldu, M, K, type)) != PATCH_OK ||
+        (st = check_rows("q", q, ldq, M, K, PATCH_INT8)) != PATCH_OK ||
+        (st = check_rows("scale", scale, 1, 1, 1, PATCH_FP32)) != PATCH_OK)
+        return st;
+    RowArgs a = {};
+    a.x = gate;
+    a.ldx = ldg;
+    a.r = up;
+    a.ldr = ldu;
+    a.M = M;
+    a.K = (int)K;
+    a.q = q;
+    a.ldq = ldq;
+    a.scale = scale;
+    return run_rows(a, kRowSiluMul, type, stream);
+}
+
+patch_status patch_dequantize_q8(const int8_t* q, int64_t ldq, const float* scale, int64_t M, int64_t K, void* out,
+                                 int64_t ldo, int type, void* stream) {
+    patch_status st = check_row_sizes(M, K, type);
+    if (st != PATCH_OK || M == 0) return st;
+    if ((st = check_rows("q", q, ldq, M, K, PATCH_INT8)) != PATCH_OK ||
+        (st = check_rows("scale", scale, 1, 1, 1, PATCH_FP32)) != PATCH_OK ||
+        (st = check_rows("out", out, ldo, M, K, type)) != PATCH_OK)
+        return st;
+    if (M == 1) ldq = ldo = 0;
+    cudaError_t e = launch_dequantize_q8(q, ldq, scale, M, (int)K, out, ldo, type, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "row kernel launch");
+    return PATCH_OK;
+}
+
 }  // extern "C"
 
 // ---------------------------------------------------------------------------
@@ -1512,9 +1860,10 @@ extern "C" patch_status patch_linear_noalloc(patch_handle h, const void* X_bf16,
                                              void* stream) {
     if (!h) return fail(PATCH_ERR_ARG, "handle is NULL");
     if (M < 0) return fail(PATCH_ERR_ARG, "M must be >= 0");
-    if (M == 0) return PATCH_OK;
-    patch_status s = check_xy(X_bf16, Y_bf16);
+    patch_status s = check_bf16(h->q8);
     if (s != PATCH_OK) return s;
+    if (M == 0) return PATCH_OK;
+    if ((s = check_xy(X_bf16, Y_bf16)) != PATCH_OK) return s;
     if (M > (int64_t)INT32_MAX / 2) return fail(PATCH_ERR_SHAPE, "M too large");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((s = check_device_is(h->device)) != PATCH_OK) return s;

@@ -1,0 +1,80 @@
+// 8-bit integer path: packed-format constants, kernel argument structs and
+// launch entry points shared by the host runtime.
+//
+// The packed format keeps the bf16 format's record sizes. A slab is a strip
+// (128 rows of W) times 128 columns: a dense slab is the 128 x 128 block of
+// codes, 128 bytes per row in the 128-byte-swizzled layout (16 KB); a 2:4
+// slab is 64 kept codes per row in the 64-byte-swizzled layout (8 KB) plus
+// its own 2 KB metadata block (one chunk per slab), 16 bytes per row: the
+// 4-bit code of group g of the slab (columns 4g .. 4g+3) at bit 4g of the
+// row's 128 bits. One tcgen05.cp.128x128b puts the block into four TMEM
+// columns, row r in lane r; each sparse MMA (K = 64) reads two of them. A
+// last slab of 64 columns (K % 128 == 64) is padded with zero codes.
+#pragma once
+
+#include "kernels.cuh"
+
+namespace patch {
+
+constexpr int kQ8SlabK = 128;
+
+// Output element types (match patch_dtype).
+constexpr int kBf16 = 0, kFp16 = 1, kFp32 = 2;
+
+struct Q8PackArgs {
+    const void* W;            // N x K, row-major: bf16 bits, or int8 codes
+    int w_int8;
+    const uint8_t* bits;      // bit-packed keep mask
+    int bitorder;             // 0 MSB first, 1 LSB first
+    const uint8_t* flags;     // tile flags on the device, (N/R) x (K/C)
+    const uint32_t* slab;     // per-strip slab table, S x KB
+    const uint32_t* meta;     // metadata block table, S x KB
+    const uint32_t* gemm;     // CTA-pair slab table, S x KB
+    float* w_scale;           // N channel scales (written for bf16 weights, read back by the pack)
+    uint8_t* out;             // packed bytes
+    int64_t K;
+    int R, C, KB;
+    unsigned long long* counters;  // [bad groups, stray zeros, pruned, bad scales]
+};
+cudaError_t launch_q8_pack(const Q8PackArgs& a, int S, cudaStream_t st);
+cudaError_t launch_q8_unpack(const uint8_t* packed, const uint32_t* slab, const uint32_t* meta, int S, int KB, int64_t K,
+                             int8_t* W, cudaStream_t st);
+
+// Per-call arguments of the products (fields as in GroupArgs).
+struct Q8Args {
+    const LinDesc* lins;
+    void* Y[kMaxGroup];
+    int64_t ldy[kMaxGroup];           // row pitch of Y, elements
+    const float* x_scale[kMaxGroup];  // M token scales
+    const float* w_scale[kMaxGroup];  // N channel scales
+    int* partial[kMaxGroup];          // split-K sums, int32
+    unsigned* counters[kMaxGroup];
+    const int* work_off;
+    const int* work;
+    int M, MB;
+    int tile_gran, tile_extra;
+    int* status;
+};
+
+cudaError_t launch_q8_gemm(const GroupMaps& maps, const Q8Args& a, int y_type, int n_tok, int grid, cudaStream_t st);
+cudaError_t q8_prepare_single();
+
+// Row operators: one row of 8-bit codes and one scale per token.
+enum RowMode { kRowQuantize = 0, kRowNorm = 1, kRowNormResidual = 2, kRowSiluMul = 3 };
+struct RowArgs {
+    const void* x;            // x, or gate
+    const void* r;            // residual, or up
+    void* ro;                 // x + residual
+    const void* gamma;
+    int64_t ldx, ldr, ldo, ldq;
+    int64_t M;
+    int K;
+    float eps;
+    int8_t* q;
+    float* scale;
+};
+cudaError_t launch_rows_q8(const RowArgs& a, int mode, int type, int sms, cudaStream_t st);
+cudaError_t launch_dequantize_q8(const int8_t* q, int64_t ldq, const float* scale, int64_t M, int K, void* out, int64_t ldo,
+                                 int type, cudaStream_t st);
+
+}  // namespace patch

@@ -16,8 +16,8 @@
  *     card, last sentence of "How to use".
  *
  * Conventions for every call:
- *   - W, X, Y are bf16, row-major (K contiguous for W and X, N contiguous
- *     for Y). "dev" pointers are CUDA device pointers on the current device;
+ *   - W, X, Y are bf16 (but for the calls under "8-bit integers"), row-major
+ *     (K contiguous for W and X, N contiguous for Y). "dev" pointers are CUDA device pointers on the current device;
  *     "host" pointers are host memory (pinned is fastest).
  *   - stream is a cudaStream_t passed as void*; NULL is the legacy default
  *     stream. Calls are stream-ordered and asynchronous unless stated.
@@ -55,7 +55,7 @@ typedef enum {
     PATCH_OK = 0,
     PATCH_ERR_ARG = 1,         /* null pointer, bad enum value, negative size */
     PATCH_ERR_SHAPE = 2,       /* a dimension does not fit the tiling rules */
-    PATCH_ERR_ALIGN = 3,       /* a pointer is not 16-byte aligned */
+    PATCH_ERR_ALIGN = 3,       /* a pointer (or a row pitch) is not aligned as the call asks */
     PATCH_ERR_MASK = 4,        /* a group inside a 2:4 tile does not keep exactly two */
     PATCH_ERR_CUDA = 5,        /* a CUDA runtime call failed */
     PATCH_ERR_TIMEOUT = 6,     /* a device-side wait ran past its limit */
@@ -104,6 +104,14 @@ typedef struct {
     int64_t stray_zeros;        /* mask zeros inside tiles flagged dense */
     double sparsity;            /* pruned / (N*K) */
 } patch_info_t;
+
+/* Element types of the 8-bit integer path. */
+typedef enum {
+    PATCH_BF16 = 0,
+    PATCH_FP16 = 1,
+    PATCH_FP32 = 2,
+    PATCH_INT8 = 3
+} patch_dtype;
 
 /*
  * patch_pack - validate the mask and build the packed weights (one-time).
@@ -412,6 +420,109 @@ void patch_free(patch_handle h);
  * Not part of the product: a check for tests and deployment health probes.
  */
 patch_status patch_selftest_wait(void* stream);
+
+/*
+ * 8-bit integers.
+ *
+ * The pages run the masked linears in bf16; these calls serve the same tiles
+ * with 8-bit weights and activations (half the weight bytes, twice the tensor
+ * rate). A row y of numbers is held as int8 codes and one fp32 scale:
+ *
+ *     scale = max(max_k |y[k]| / 127, 2^-126)     code[k] = round(y[k] / scale)
+ *
+ * (ties to even; codes in -127..127), and stands for code * scale. Activations
+ * have one scale per token, weights one per output channel. A row that holds a
+ * NaN or an infinity, or whose norm's sum of squares overflows fp32, gets the
+ * scale NaN and zero codes: what is computed from it is NaN.
+ *
+ * Matrices have rows of contiguous elements and a row pitch (ld, in elements,
+ * at least the row's length; ignored for one row). Unless a call says more,
+ * pointers need the alignment of their elements only; rows of 16-byte multiples
+ * on 16-byte boundaries are fastest. Outputs must not overlap inputs, except
+ * where a call says so. M == 0 is a no-op. No call but patch_pack_q8
+ * synchronises or, after the first call for an M, allocates.
+ */
+
+/*
+ * patch_pack_q8 - patch_pack for 8-bit weights.
+ *
+ *   W        dev, N*K row-major, 16-byte aligned: bf16 (w_type PATCH_BF16; each
+ *            channel is quantised over its kept weights) or int8 codes (w_type
+ *            PATCH_INT8). Not retained.
+ *   w_scale  dev, N fp32: the channel scales of int8 codes (copied); NULL for
+ *            bf16 weights.
+ *   N, K, mask_bits, bitorder, tile_flags, tile_rows, tile_cols, stream, out
+ *            as for patch_pack; K <= 131008, so that the int32 sums of any
+ *            codes are exact.
+ * The handle works with patch_linear_q8, patch_unpack_q8, patch_info,
+ * patch_copy_packed (whose tables then have KB = KC = ceil(K/128)), patch_check,
+ * patch_free, patch_group_create (with other 8-bit handles) and
+ * patch_group_path; the bf16 calls refuse it (PATCH_ERR_ARG). A bf16 channel
+ * that keeps a NaN or an infinity gives PATCH_ERR_ARG.
+ */
+patch_status patch_pack_q8(const void* W, int w_type, const float* w_scale, int64_t N, int64_t K,
+                           const uint8_t* mask_bits, int bitorder, const uint8_t* tile_flags, int tile_rows,
+                           int tile_cols, void* stream, patch_handle* out);
+
+/*
+ * patch_linear_q8 - Y[m,n] = (sum_k X[m,k] W[n,k]) * x_scale[m] * w_scale[n]
+ * over the packed (masked) codes of h: an exact int32 sum, the two scales in
+ * fp32, one rounding to the output type.
+ *
+ *   X        dev, M rows of K codes, 16-byte aligned, pitch ldx a multiple of 16.
+ *   x_scale  dev, M fp32.
+ *   Y        dev, M rows of N elements of y_type (PATCH_BF16, PATCH_FP16 or
+ *            PATCH_FP32), 16-byte aligned, pitch ldy a multiple of 16 bytes.
+ *            Every element of the N columns is written, nothing beside them.
+ *   path     PATCH_PATH_AUTO, or a kernel of patch_path that has an 8-bit form
+ *            (PATCH_ERR_UNSUPPORTED for the others): GEMM_SINGLE.
+ * Schedules, workspaces, capture and concurrency as for patch_linear.
+ */
+patch_status patch_linear_q8(patch_handle h, const int8_t* X, int64_t ldx, const float* x_scale, int64_t M, void* Y,
+                             int64_t ldy, int y_type, int path, void* stream);
+
+/*
+ * patch_group_linear_q8 - patch_linear_q8 for every member of a group of 8-bit
+ * handles in one launch. Host arrays of one entry per member; ldx or ldy NULL:
+ * contiguous rows. Members may share X and x_scale.
+ */
+patch_status patch_group_linear_q8(patch_group g, const int8_t* const* X, const int64_t* ldx,
+                                   const float* const* x_scale, int64_t M, void* const* Y, const int64_t* ldy,
+                                   int y_type, int path, void* stream);
+
+/* patch_unpack_q8 - the masked codes (N*K int8, dev, row-major, 16-byte aligned)
+ * and the N channel scales (fp32, dev) of a handle. */
+patch_status patch_unpack_q8(patch_handle h, int8_t* W, float* w_scale, void* stream);
+
+/*
+ * patch_quantize_q8 - the codes and scales of the rows of x.
+ *   x      dev, M rows of K elements of `type` (PATCH_BF16, PATCH_FP16, PATCH_FP32).
+ *   q      dev, M rows of K codes.   scale  dev, M fp32.
+ */
+patch_status patch_quantize_q8(const void* x, int64_t ldx, int type, int64_t M, int64_t K, int8_t* q, int64_t ldq,
+                               float* scale, void* stream);
+
+/*
+ * patch_rmsnorm_q8 - the codes and scales of h / sqrt(mean(h^2) + eps) * gamma,
+ * with h = x, or h = x + residual rounded to `type` and written to residual_out.
+ *   residual, residual_out  dev, M rows of K, or both NULL. residual_out may be
+ *          x or residual itself (same pointer and pitch).
+ *   gamma  dev, K elements of `type`.
+ * The sum of squares and the norm are fp32; they see the rounded h.
+ */
+patch_status patch_rmsnorm_q8(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* residual_out,
+                              int64_t ldo, const void* gamma, int type, float eps, int64_t M, int64_t K, int8_t* q,
+                              int64_t ldq, float* scale, void* stream);
+
+/* patch_silu_mul_q8 - the codes and scales of gate / (1 + exp(-gate)) * up. gate
+ * and up may be the two halves of one matrix. */
+patch_status patch_silu_mul_q8(const void* gate, int64_t ldg, const void* up, int64_t ldu, int type, int64_t M,
+                               int64_t K, int8_t* q, int64_t ldq, float* scale, void* stream);
+
+/* patch_dequantize_q8 - the values code * scale of the rows of q, rounded once to
+ * `type`. */
+patch_status patch_dequantize_q8(const int8_t* q, int64_t ldq, const float* scale, int64_t M, int64_t K, void* out,
+                                 int64_t ldo, int type, void* stream);
 
 /* Message of the last failed call on this thread ("" if none). */
 const char* patch_last_error(void);
