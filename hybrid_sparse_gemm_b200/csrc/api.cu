@@ -104,7 +104,7 @@ patch_status prepare_device(int* dev_out, DeviceInfo* info_out) {
         PATCH_CUDA(gemm_prepare_wide(&di.wide_clusters));
         if (di.wide_clusters <= 0) di.wide_clusters = 1;
         PATCH_CUDA(decode_prepare());
-        PATCH_CUDA(q8_prepare_single());
+        PATCH_CUDA(q8_prepare_split());
         if (di.pair_clusters <= 0) di.pair_clusters = 1;
         it = g_dev.emplace(dev, di).first;
     }
@@ -937,56 +937,82 @@ patch_status run_group(patch_group g, const void* const* X, int64_t M, void* con
     return PATCH_OK;
 }
 
-// The kernel an 8-bit call runs. GEMM_SINGLE: any M.
+// The kernel an 8-bit call runs: the split-K kernel with 16- or 64-token units
+// (GEMV, M <= 64) or with 128-token units (GEMM_SINGLE, any M).
 patch_status resolve_path_q8(patch_group g, int path, int64_t M, int* out) {
     (void)g;
-    (void)M;
-    if (path == PATCH_PATH_AUTO || path == PATCH_PATH_GEMM) path = PATCH_PATH_GEMM_SINGLE;
-    if (path != PATCH_PATH_GEMM_SINGLE) return fail(PATCH_ERR_UNSUPPORTED, "path %d has no 8-bit kernel", path);
+    if (path == PATCH_PATH_AUTO) path = M <= kDecodeWideBN ? PATCH_PATH_GEMV : PATCH_PATH_GEMM_SINGLE;
+    if (path == PATCH_PATH_GEMM) path = PATCH_PATH_GEMM_SINGLE;
+    if (path != PATCH_PATH_GEMV && path != PATCH_PATH_GEMM_SINGLE)
+        return fail(PATCH_ERR_UNSUPPORTED, "path %d has no 8-bit kernel", path);
+    if (path == PATCH_PATH_GEMV && M > kDecodeWideBN)
+        return fail(PATCH_ERR_SHAPE, "the decode kernel takes M <= %d (got %lld)", kDecodeWideBN, (long long)M);
     *out = path;
     return PATCH_OK;
 }
 
-// One launch over every member of an 8-bit group.
-patch_status run_group_q8(patch_group g, const int8_t* const* X, const int64_t* ldx, const float* const* x_scale,
-                          int64_t M, void* const* Y, const int64_t* ldy, int y_type, int path, cudaStream_t st) {
-    patch_status s = resolve_path_q8(g, path, M, &path);
-    if (s != PATCH_OK) return s;
-    const int kernel = kQ8Kernel;
-    const int bn = kernel_bn(kernel);
-    const int mb = (int)((M + bn - 1) / bn);
-    const int n_tok = (int)std::min<int64_t>(bn, (M + 15) & ~(int64_t)15);  // tokens per MMA and per activation box
-    GroupMaps maps;
-    Q8Args a;
-    memset(&maps, 0, sizeof(maps));
-    memset(&a, 0, sizeof(a));
+// The operands of an 8-bit call, one entry per member.
+struct Q8Call {
+    const int8_t* const* X;
+    const int64_t* ldx;           // NULL: contiguous
+    const float* const* x_scale;
+    int64_t M;
+    void* const* Y;
+    const int64_t* ldy;           // NULL: contiguous
+    int y_type;
+    // a single row needs no pitch, but its tensor map wants a multiple of 16 bytes
+    int64_t pitch_x(int l, int64_t K) const { return M == 1 ? (K + 15) & ~(int64_t)15 : ldx ? ldx[l] : K; }
+    int64_t pitch_y(int l, int64_t N) const { return ldy ? ldy[l] : N; }
+};
+
+template <int G>
+patch_status run_q8_split(patch_group g, const Q8Call& c, int path, cudaStream_t st) {
+    const int bn = path == PATCH_PATH_GEMM_SINGLE ? kGemmBN : c.M <= kDecodeBN ? kDecodeBN : kDecodeWideBN;
+    Q8Maps<G> maps;
+    Q8SplitArgs<G> a;
+    // token tiles of equal size, a multiple of 16
+    const int64_t mb = (c.M + bn - 1) / bn;
+    a.n_tok = (int)(((c.M + mb - 1) / mb + 15) & ~(int64_t)15);
+    a.MB = (int)((c.M + a.n_tok - 1) / a.n_tok);
+    a.M = (int)c.M;
+    a.n = g->n;
+    a.status = g->status_dev;
+    int64_t units = 0;
+    int kb = 8;
     for (int l = 0; l < g->n; ++l) {
         patch_handle h = g->h[l];
-        if (kernel_rows(h->plan, kernel) * mb > kUnitMask)
-            return fail(PATCH_ERR_SHAPE, "M=%lld gives more than %d output tiles", (long long)M, kUnitMask);
-        // a single row needs no pitch, but the map wants a multiple of 16 bytes
-        const int64_t pitch = M == 1 ? (h->K + 15) & ~(int64_t)15 : ldx ? ldx[l] : h->K;
-        if ((s = encode_codes(&maps.x[l], X[l], h->K, M, pitch, n_tok)) != PATCH_OK) return s;
-        maps.a32[l] = h->tm_a32;
+        patch_status s = encode_codes(&maps.x[l], c.X[l], h->K, c.M, c.pitch_x(l, h->K), a.n_tok);
+        if (s != PATCH_OK) return s;
         maps.a16[l] = h->tm_a16;
         maps.a8[l] = h->tm_a8;
         maps.e[l] = h->tm_e;
-        a.Y[l] = Y[l];
-        a.ldy[l] = ldy ? ldy[l] : h->N;
-        a.x_scale[l] = x_scale[l];
-        a.w_scale[l] = h->w_scale;
+        Q8Member& m = a.m[l];
+        m.slab = h->slab_dev;
+        m.meta = h->meta_dev;
+        m.x_scale = c.x_scale[l];
+        m.w_scale = h->w_scale;
+        m.Y = c.Y[l];
+        m.ldy = c.pitch_y(l, h->N);
+        m.KB = h->plan.KB;
+        m.unit0 = (int)units;
+        units += (int64_t)h->plan.S * a.MB;
+        if (units > INT32_MAX / 8)
+            return fail(PATCH_ERR_SHAPE, "M=%lld gives more than %d output tiles", (long long)c.M, INT32_MAX / 8);
+        kb = std::min(kb, h->plan.KB);
     }
-    WorkList* wl = nullptr;
-    if ((s = get_worklist(g, kernel, mb, st, &wl)) != PATCH_OK) return s;
-    a.lins = g->lins_dev;
-    a.work_off = wl->off;
-    a.work = wl->work;
-    a.M = (int)M;
-    a.MB = mb;
-    a.status = g->status_dev;
-    cudaError_t e = launch_q8_gemm(maps, a, y_type, n_tok, wl->grid, st);
+    // Parts of K: as many as keep every CTA resident (two per SM), at least one slab each.
+    a.P = 8;
+    while (a.P > 1 && (units * a.P > 4 * (int64_t)g->dev.sms || a.P > kb)) a.P /= 2;
+    const cudaError_t e = launch_q8_split<G>(maps, a, bn, c.y_type, (int)units * a.P, st);
     if (e != cudaSuccess) return cuda_fail(e, "8-bit kernel launch");
     return PATCH_OK;
+}
+
+// One launch over every member of an 8-bit group.
+patch_status run_group_q8(patch_group g, const Q8Call& c, int path, cudaStream_t st) {
+    patch_status s = resolve_path_q8(g, path, c.M, &path);
+    if (s != PATCH_OK) return s;
+    return g->n == 1 ? run_q8_split<1>(g, c, path, st) : run_q8_split<kMaxGroup>(g, c, path, st);
 }
 
 int64_t type_size(int type) { return type == PATCH_FP32 ? 4 : type == PATCH_INT8 ? 1 : 2; }
@@ -1693,7 +1719,7 @@ patch_status patch_linear_q8(patch_handle h, const int8_t* X, int64_t ldx, const
     if (M == 0) return PATCH_OK;
     if ((st = check_q8(h, X, ldx, x_scale, M, Y, ldy, y_type)) != PATCH_OK) return st;
     if ((st = check_device_is(h->device)) != PATCH_OK) return st;
-    return run_group_q8(h->self, &X, &ldx, &x_scale, M, &Y, &ldy, y_type, path, static_cast<cudaStream_t>(stream));
+    return run_group_q8(h->self, {&X, &ldx, &x_scale, M, &Y, &ldy, y_type}, path, static_cast<cudaStream_t>(stream));
 }
 
 patch_status patch_group_linear_q8(patch_group g, const int8_t* const* X, const int64_t* ldx,
@@ -1710,7 +1736,7 @@ patch_status patch_group_linear_q8(patch_group g, const int8_t* const* X, const 
             return st;
     }
     if ((st = check_device_is(g->device)) != PATCH_OK) return st;
-    return run_group_q8(g, X, ldx, x_scale, M, Y, ldy, y_type, path, static_cast<cudaStream_t>(stream));
+    return run_group_q8(g, {X, ldx, x_scale, M, Y, ldy, y_type}, path, static_cast<cudaStream_t>(stream));
 }
 
 patch_status patch_unpack_q8(patch_handle h, int8_t* W, float* w_scale, void* stream) {

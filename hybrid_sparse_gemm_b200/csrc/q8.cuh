@@ -40,24 +40,39 @@ cudaError_t launch_q8_pack(const Q8PackArgs& a, int S, cudaStream_t st);
 cudaError_t launch_q8_unpack(const uint8_t* packed, const uint32_t* slab, const uint32_t* meta, int S, int KB, int64_t K,
                              int8_t* W, cudaStream_t st);
 
-// Per-call arguments of the products (fields as in GroupArgs).
-struct Q8Args {
-    const LinDesc* lins;
-    void* Y[kMaxGroup];
-    int64_t ldy[kMaxGroup];           // row pitch of Y, elements
-    const float* x_scale[kMaxGroup];  // M token scales
-    const float* w_scale[kMaxGroup];  // N channel scales
-    int* partial[kMaxGroup];          // split-K sums, int32
-    unsigned* counters[kMaxGroup];
-    const int* work_off;
-    const int* work;
-    int M, MB;
-    int tile_gran, tile_extra;
-    int* status;
+// Tensor maps of G members: activation codes (per call), and the packed bytes
+// viewed as 128-byte rows with 128-, 64- and 16-row boxes.
+template <int G>
+struct Q8Maps {
+    CUtensorMap x[G], a16[G], a8[G], e[G];
 };
 
-cudaError_t launch_q8_gemm(const GroupMaps& maps, const Q8Args& a, int y_type, int n_tok, int grid, cudaStream_t st);
-cudaError_t q8_prepare_single();
+// Split-K kernel: one cluster of P CTAs per unit (strip, token tile).
+struct Q8Member {
+    const uint32_t* slab;  // S x KB
+    const uint32_t* meta;  // S x KB
+    const float* x_scale;  // M
+    const float* w_scale;  // N
+    void* Y;
+    int64_t ldy;           // row pitch of Y, elements
+    int KB;
+    int unit0;             // the member's first unit
+};
+template <int G>
+struct Q8SplitArgs {
+    Q8Member m[G];
+    int* status;
+    int n;      // members
+    int M;
+    int MB;     // token tiles
+    int n_tok;  // tokens per tile, a multiple of 16
+    int P;      // CTAs per unit
+};
+// grid: all units * P; bn: 16, 64 or 128 (n_tok at most)
+template <int G>
+cudaError_t launch_q8_split(const Q8Maps<G>& maps, const Q8SplitArgs<G>& a, int bn, int y_type, int grid,
+                            cudaStream_t st);
+cudaError_t q8_prepare_split();
 
 // Row operators: one row of 8-bit codes and one scale per token.
 enum RowMode { kRowQuantize = 0, kRowNorm = 1, kRowNormResidual = 2, kRowSiluMul = 3 };

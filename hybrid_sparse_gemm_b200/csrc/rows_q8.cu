@@ -139,6 +139,8 @@ __global__ void __launch_bounds__(1024) rows_kernel(const RowArgs a) {
     __shared__ uint32_t s_max[32];
     __shared__ float s_sum[32];
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (row >= a.M) return;  // whole warps: rows of a block's y share no barrier
     const int n = blockDim.x;
     float v[ITEMS > 0 ? ITEMS : 1][VEC];
@@ -218,6 +220,22 @@ __global__ void __launch_bounds__(1024) rows_kernel(const RowArgs a) {
     }
 }
 
+// A launch whose set-up may overlap the stream's previous kernel (the kernels
+// wait for it before they touch memory).
+template <class... Params, class... Args>
+cudaError_t go(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <class T, int MODE>
 cudaError_t launch_rows(const RowArgs& a, int sms, cudaStream_t st) {
     auto wide = [](const void* p, int64_t ld) {
@@ -227,42 +245,43 @@ cudaError_t launch_rows(const RowArgs& a, int sms, cudaStream_t st) {
                      ((reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)a.ldq) & 7u) == 0;
     const int64_t items = vec ? a.K / 8 : a.K;  // vectors in a row
     dim3 block(32, 1), grid((unsigned)a.M);
+    cudaError_t e = cudaSuccess;
     auto per_row = [&](int each) { return (int)((items + each - 1) / each + 31) / 32 * 32; };
     if (vec) {
         if (items <= 128) {
             block.y = (unsigned)(a.M < 8 ? a.M : 8);
             grid.x = (unsigned)((a.M + block.y - 1) / block.y);
-            if (items <= 32) rows_kernel<T, MODE, 8, 1><<<grid, block, 0, st>>>(a);
-            else if (items <= 64) rows_kernel<T, MODE, 8, 2><<<grid, block, 0, st>>>(a);
-            else rows_kernel<T, MODE, 8, 4><<<grid, block, 0, st>>>(a);
-            return cudaGetLastError();
+            if (items <= 32) e = go(rows_kernel<T, MODE, 8, 1>, grid, block, st, a);
+            else if (items <= 64) e = go(rows_kernel<T, MODE, 8, 2>, grid, block, st, a);
+            else e = go(rows_kernel<T, MODE, 8, 4>, grid, block, st, a);
+            return e;
         }
         const int most = a.M <= sms ? 1024 : 512;
         if (per_row(1) <= most) {
             block.x = per_row(1);
-            rows_kernel<T, MODE, 8, 1><<<grid, block, 0, st>>>(a);
+            e = go(rows_kernel<T, MODE, 8, 1>, grid, block, st, a);
         } else if (per_row(2) <= most) {
             block.x = per_row(2);
-            rows_kernel<T, MODE, 8, 2><<<grid, block, 0, st>>>(a);
+            e = go(rows_kernel<T, MODE, 8, 2>, grid, block, st, a);
         } else if (per_row(4) <= 1024) {
             block.x = per_row(4);
-            rows_kernel<T, MODE, 8, 4><<<grid, block, 0, st>>>(a);
+            e = go(rows_kernel<T, MODE, 8, 4>, grid, block, st, a);
         } else {
             block.x = 1024;
-            rows_kernel<T, MODE, 8, 0><<<grid, block, 0, st>>>(a);
+            e = go(rows_kernel<T, MODE, 8, 0>, grid, block, st, a);
         }
     } else if (items <= 32 * 16) {
         block.y = (unsigned)(a.M < 8 ? a.M : 8);
         grid.x = (unsigned)((a.M + block.y - 1) / block.y);
-        rows_kernel<T, MODE, 1, 16><<<grid, block, 0, st>>>(a);
+        e = go(rows_kernel<T, MODE, 1, 16>, grid, block, st, a);
     } else if (items <= 1024 * 16) {
         block.x = per_row(16);
-        rows_kernel<T, MODE, 1, 16><<<grid, block, 0, st>>>(a);
+        e = go(rows_kernel<T, MODE, 1, 16>, grid, block, st, a);
     } else {
         block.x = 1024;
-        rows_kernel<T, MODE, 1, 0><<<grid, block, 0, st>>>(a);
+        e = go(rows_kernel<T, MODE, 1, 0>, grid, block, st, a);
     }
-    return cudaGetLastError();
+    return e;
 }
 
 template <class T>
@@ -277,6 +296,8 @@ cudaError_t launch_rows_type(const RowArgs& a, int mode, int sms, cudaStream_t s
 template <class T, int VEC>
 __global__ void __launch_bounds__(256) dequantize_kernel(const int8_t* q, int64_t ldq, const float* scale, int K,
                                                          int chunks, T* out, int64_t ldo) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t row = blockIdx.x / chunks;
     const int e = ((int)(blockIdx.x % chunks) * 256 + (int)threadIdx.x) * VEC;
     if (e >= K) return;
@@ -305,11 +326,8 @@ cudaError_t launch_deq(const int8_t* q, int64_t ldq, const float* scale, int64_t
     const int64_t most = 2147483647ll / chunks;
     for (int64_t m0 = 0; m0 < M; m0 += most) {
         const unsigned grid = (unsigned)((M - m0 < most ? M - m0 : most) * chunks);
-        if (vec)
-            dequantize_kernel<T, 8><<<grid, 256, 0, st>>>(q + m0 * ldq, ldq, scale + m0, K, chunks, out + m0 * ldo, ldo);
-        else
-            dequantize_kernel<T, 1><<<grid, 256, 0, st>>>(q + m0 * ldq, ldq, scale + m0, K, chunks, out + m0 * ldo, ldo);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = go(vec ? dequantize_kernel<T, 8> : dequantize_kernel<T, 1>, dim3(grid), dim3(256), st,
+                                 q + m0 * ldq, ldq, scale + m0, K, chunks, out + m0 * ldo, ldo);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
