@@ -81,6 +81,7 @@ patch_status check_flags(const uint8_t* flags, int64_t n) {
 struct DeviceInfo {
     int sms = 0;
     int pair_clusters = 0;  // co-resident 2-CTA clusters of the pair kernel
+    int q8_wide_clusters = 0;  // the same of its 8-bit counterpart
     int wide_clusters = 0;  // co-resident CTA pairs of the two-strips-per-CTA kernel
 };
 std::mutex g_dev_mu;
@@ -105,6 +106,8 @@ patch_status prepare_device(int* dev_out, DeviceInfo* info_out) {
         if (di.wide_clusters <= 0) di.wide_clusters = 1;
         PATCH_CUDA(decode_prepare());
         PATCH_CUDA(q8_prepare_split());
+        PATCH_CUDA(q8_prepare_wide(&di.q8_wide_clusters));
+        if (di.q8_wide_clusters <= 0) di.q8_wide_clusters = 1;
         if (di.pair_clusters <= 0) di.pair_clusters = 1;
         it = g_dev.emplace(dev, di).first;
     }
@@ -262,10 +265,11 @@ std::vector<int> pair_order(const std::vector<uint8_t>& sp, int S, int KB) {
 
 // Region V (every slab), region E (a metadata block per chunk holding a 2:4
 // slab), region D (dense images of 2:4 slabs whose partner strip is dense).
-// slab_k: columns per slab, per_chunk: slabs that share a metadata block (64
-// and 2 for bf16, 128 and 1 for 8-bit codes, whose last slab may be half).
-void build_plan(Plan& p, int64_t N, int64_t K, int R, int C, const uint8_t* flags, int slab_k = kSlabK,
-                int per_chunk = 2) {
+// 8-bit codes: slabs of 128 columns (the last may be half), each with its own
+// metadata block, which follows its values in region V; no region E.
+void build_plan(Plan& p, int64_t N, int64_t K, int R, int C, const uint8_t* flags, bool q8 = false) {
+    const int slab_k = q8 ? kQ8SlabK : kSlabK;
+    const int per_chunk = q8 ? 1 : 2;  // slabs that share a metadata block
     p.S = (int)(N / kStrip);
     p.KB = (int)((K + slab_k - 1) / slab_k);
     p.KC = (p.KB + per_chunk - 1) / per_chunk;
@@ -298,7 +302,8 @@ void build_plan(Plan& p, int64_t N, int64_t K, int R, int C, const uint8_t* flag
             const bool first = x && (b % per_chunk == 0 || !is_sp(s, b - 1));
             p.slab[(size_t)s * p.KB + b] =
                 (uint32_t)((off / 16) << 2) | (first ? kSlabFirst : 0u) | (x ? kSlabSparse : 0u);
-            off += x ? kSparseValBytes : kDenseSlabBytes;
+            if (q8 && x) p.meta[(size_t)s * p.KC + b] = (uint32_t)((off + kSparseValBytes) / 16);
+            off += !x ? kDenseSlabBytes : q8 ? kQ8SparseBytes : kSparseValBytes;
             p.sparse += x;
             p.strip_cost[s] += x ? 0.5 : 1.0;
             p.strip_bytes[s] += x ? kSparseValBytes : kDenseSlabBytes;
@@ -308,8 +313,10 @@ void build_plan(Plan& p, int64_t N, int64_t K, int R, int C, const uint8_t* flag
             bool any = false;
             for (int b = c * per_chunk; b < std::min(p.KB, (c + 1) * per_chunk); ++b) any = any || is_sp(s, b);
             if (any) {
-                p.meta[(size_t)s * p.KC + c] = (uint32_t)(off / 16);
-                off += kMetaBytes;
+                if (!q8) {
+                    p.meta[(size_t)s * p.KC + c] = (uint32_t)(off / 16);
+                    off += kMetaBytes;
+                }
                 ++p.meta_blocks;
                 p.strip_bytes[s] += kMetaBytes;
             }
@@ -389,6 +396,7 @@ struct patch_handle_s {
     std::mutex groups_mu;
     std::vector<patch_group_s*> groups;   // groups this handle belongs to (its own one-member group too)
     CUtensorMap tm_a32, tm_a16, tm_a8, tm_e;
+    CUtensorMap tm_a10;         // 2:4 records of 8-bit codes
     patch_info_t info{};
     patch_group_s* self = nullptr;        // one-member group used by patch_linear
     std::mutex mu;
@@ -650,12 +658,11 @@ patch_status get_decode_ws(patch_group g, cudaStream_t st, int bn, const DecodeW
 // MMAs, 4 CTA pair with two strips per CTA, 5 decode with 64-token MMAs):
 // tokens per tile,
 // activation rows per TMA box, weight rows of a work unit, persistent slots.
-// 8-bit kernels: 10 + the number of their bf16 counterpart.
-constexpr int kQ8Kernel = 10;
+// The 8-bit kernel that runs a schedule: CTA pair with two strips per CTA.
+constexpr int kQ8Wide = 14;
 constexpr int64_t kQ8MaxK = 131008;  // K * 128 * 128 stays below 2^31
 
 int kernel_bn(int kernel) {
-    kernel %= kQ8Kernel;
     return kernel == 0   ? kGemmBN
            : kernel == 2 ? kDecodeBN
            : kernel == 5 ? kDecodeWideBN
@@ -666,12 +673,11 @@ int kernel_box_rows(int kernel) {
     return kernel == 1 ? kGemm2BN / 2 : kernel == 4 ? kGemm22BN / 2 : kernel_bn(kernel);
 }
 int64_t kernel_rows(const Plan& p, int kernel) {
-    kernel %= kQ8Kernel;
     const int64_t pairs = (int64_t)p.pair_cost.size();
     return kernel == 0 ? (int64_t)p.strip_cost.size() : kernel == 1 ? pairs : (pairs + 1) / 2;
 }
 int kernel_slots(const DeviceInfo& d, int kernel) {
-    kernel %= kQ8Kernel;
+    if (kernel == kQ8Wide) return d.q8_wide_clusters;
     return kernel == 1   ? d.pair_clusters
            : kernel == 4 ? d.wide_clusters
            : kernel == 2 ? kDecodeCtasPerSm * d.sms
@@ -686,7 +692,7 @@ void lpt_schedule(patch_group g, int kernel, int mb, std::vector<int>& off, std:
     };
     std::vector<Unit> units;
     const int slots = kernel_slots(g->dev, kernel);
-    kernel %= kQ8Kernel;
+    if (kernel == kQ8Wide) kernel = 4;
     for (int l = 0; l < g->n; ++l) {
         const Plan& p = g->h[l]->plan;
         if (kernel == 0 || kernel == 1) {
@@ -938,12 +944,17 @@ patch_status run_group(patch_group g, const void* const* X, int64_t M, void* con
 }
 
 // The kernel an 8-bit call runs: the split-K kernel with 16- or 64-token units
-// (GEMV, M <= 64) or with 128-token units (GEMM_SINGLE, any M).
+// (GEMV, M <= 64) or with 128-token units (GEMM_SINGLE, any M), or CTA pairs
+// with two strips per CTA (GEMM_WIDE, any M).
 patch_status resolve_path_q8(patch_group g, int path, int64_t M, int* out) {
-    (void)g;
-    if (path == PATCH_PATH_AUTO) path = M <= kDecodeWideBN ? PATCH_PATH_GEMV : PATCH_PATH_GEMM_SINGLE;
-    if (path == PATCH_PATH_GEMM) path = PATCH_PATH_GEMM_SINGLE;
-    if (path != PATCH_PATH_GEMV && path != PATCH_PATH_GEMM_SINGLE)
+    if (path == PATCH_PATH_AUTO) path = M <= kDecodeWideBN ? PATCH_PATH_GEMV : PATCH_PATH_GEMM;
+    if (path == PATCH_PATH_GEMM) {
+        int64_t quads = 0;
+        for (int l = 0; l < g->n; ++l) quads += (g->h[l]->plan.S + 3) / 4;
+        path = quads * ((M + kQ8WideBN - 1) / kQ8WideBN) >= g->dev.q8_wide_clusters ? PATCH_PATH_GEMM_WIDE
+                                                                                   : PATCH_PATH_GEMM_SINGLE;
+    }
+    if (path != PATCH_PATH_GEMV && path != PATCH_PATH_GEMM_SINGLE && path != PATCH_PATH_GEMM_WIDE)
         return fail(PATCH_ERR_UNSUPPORTED, "path %d has no 8-bit kernel", path);
     if (path == PATCH_PATH_GEMV && M > kDecodeWideBN)
         return fail(PATCH_ERR_SHAPE, "the decode kernel takes M <= %d (got %lld)", kDecodeWideBN, (long long)M);
@@ -984,11 +995,9 @@ patch_status run_q8_split(patch_group g, const Q8Call& c, int path, cudaStream_t
         patch_status s = encode_codes(&maps.x[l], c.X[l], h->K, c.M, c.pitch_x(l, h->K), a.n_tok);
         if (s != PATCH_OK) return s;
         maps.a16[l] = h->tm_a16;
-        maps.a8[l] = h->tm_a8;
-        maps.e[l] = h->tm_e;
+        maps.a10[l] = h->tm_a10;
         Q8Member& m = a.m[l];
         m.slab = h->slab_dev;
-        m.meta = h->meta_dev;
         m.x_scale = c.x_scale[l];
         m.w_scale = h->w_scale;
         m.Y = c.Y[l];
@@ -1008,10 +1017,50 @@ patch_status run_q8_split(patch_group g, const Q8Call& c, int path, cudaStream_t
     return PATCH_OK;
 }
 
+template <int G>
+patch_status run_q8_wide(patch_group g, const Q8Call& c, cudaStream_t st) {
+    Q8Maps<G> maps;
+    Q8WideArgs<G> a;
+    // token tiles that share M's 32-token granules evenly
+    const int64_t gran = (c.M + 31) / 32, mb = (c.M + kQ8WideBN - 1) / kQ8WideBN;
+    a.M = (int)c.M;
+    a.MB = (int)mb;
+    a.tile_gran = (int)(gran / mb);
+    a.tile_extra = (int)(gran % mb);
+    a.x_rows = 16 * (a.tile_gran + (a.tile_extra ? 1 : 0));
+    a.status = g->status_dev;
+    patch_status s;
+    for (int l = 0; l < g->n; ++l) {
+        patch_handle h = g->h[l];
+        if ((h->plan.S + 3) / 4 * mb > kUnitMask)
+            return fail(PATCH_ERR_SHAPE, "M=%lld gives more than %d output tiles", (long long)c.M, kUnitMask);
+        if ((s = encode_codes(&maps.x[l], c.X[l], h->K, c.M, c.pitch_x(l, h->K), a.x_rows)) != PATCH_OK) return s;
+        maps.a16[l] = h->tm_a16;
+        maps.a10[l] = h->tm_a10;
+        Q8WideMember& m = a.m[l];
+        m.gemm = h->pgemm_dev;
+        m.order = h->order_dev;
+        m.x_scale = c.x_scale[l];
+        m.w_scale = h->w_scale;
+        m.Y = c.Y[l];
+        m.ldy = c.pitch_y(l, h->N);
+        m.S = h->plan.S;
+        m.KB = h->plan.KB;
+    }
+    WorkList* wl = nullptr;
+    if ((s = get_worklist(g, kQ8Wide, (int)mb, st, &wl)) != PATCH_OK) return s;
+    a.work_off = wl->off;
+    a.work = wl->work;
+    const cudaError_t e = launch_q8_wide<G>(maps, a, c.y_type, wl->grid, st);
+    if (e != cudaSuccess) return cuda_fail(e, "8-bit kernel launch");
+    return PATCH_OK;
+}
+
 // One launch over every member of an 8-bit group.
 patch_status run_group_q8(patch_group g, const Q8Call& c, int path, cudaStream_t st) {
     patch_status s = resolve_path_q8(g, path, c.M, &path);
     if (s != PATCH_OK) return s;
+    if (path == PATCH_PATH_GEMM_WIDE) return g->n == 1 ? run_q8_wide<1>(g, c, st) : run_q8_wide<kMaxGroup>(g, c, st);
     return g->n == 1 ? run_q8_split<1>(g, c, path, st) : run_q8_split<kMaxGroup>(g, c, path, st);
 }
 
@@ -1245,7 +1294,7 @@ patch_status pack_weights(const void* W_bf16, bool q8, const float* w_scale, int
     h->R = tile_rows;
     h->C = tile_cols;
     h->q8 = q8;
-    build_plan(h->plan, N, K, tile_rows, tile_cols, tile_flags, q8 ? kQ8SlabK : kSlabK, q8 ? 1 : 2);
+    build_plan(h->plan, N, K, tile_rows, tile_cols, tile_flags, q8);
     const Plan& p = h->plan;
     if (p.bytes / 16 >= ((int64_t)1 << 30)) {
         free_handle(h);
@@ -1279,12 +1328,14 @@ patch_status pack_weights(const void* W_bf16, bool q8, const float* w_scale, int
     }
     // tensor maps of the packed bytes viewed as rows of 64 bf16 (128 bytes):
     // two adjacent dense records (256 rows), a dense slab / dense image or two
-    // adjacent 2:4 records (128 rows), 2:4 values (64 rows), metadata (16 rows)
+    // adjacent 2:4 records (128 rows), 2:4 values (64 rows), metadata (16 rows),
+    // 2:4 codes with their metadata (80 rows)
     const int64_t rows = std::max<int64_t>(p.bytes, 2048) / 128;
     if ((st = encode_2d(&h->tm_a32, h->packed, 64, rows, 64, 256, CU_TENSOR_MAP_SWIZZLE_NONE)) != PATCH_OK ||
         (st = encode_2d(&h->tm_a16, h->packed, 64, rows, 64, 128, CU_TENSOR_MAP_SWIZZLE_NONE)) != PATCH_OK ||
         (st = encode_2d(&h->tm_a8, h->packed, 64, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_NONE)) != PATCH_OK ||
-        (st = encode_2d(&h->tm_e, h->packed, 64, rows, 64, 16, CU_TENSOR_MAP_SWIZZLE_NONE)) != PATCH_OK)
+        (st = encode_2d(&h->tm_e, h->packed, 64, rows, 64, 16, CU_TENSOR_MAP_SWIZZLE_NONE)) != PATCH_OK ||
+        (st = encode_2d(&h->tm_a10, h->packed, 64, rows, 64, 80, CU_TENSOR_MAP_SWIZZLE_NONE)) != PATCH_OK)
         return cleanup(st);
     cudaError_t e;
     if ((e = cudaMemcpyAsync(h->slab_dev, p.slab.data(), sizeof(uint32_t) * p.slab.size(), cudaMemcpyHostToDevice,
@@ -1313,7 +1364,6 @@ patch_status pack_weights(const void* W_bf16, bool q8, const float* w_scale, int
         a.bitorder = bitorder;
         a.flags = flags_dev;
         a.slab = h->slab_dev;
-        a.meta = h->meta_dev;
         a.gemm = h->gemm_dev;
         a.w_scale = h->w_scale;
         a.out = h->packed;
@@ -1747,7 +1797,7 @@ patch_status patch_unpack_q8(patch_handle h, int8_t* W, float* w_scale, void* st
     patch_status st = check_device_is(h->device);
     if (st != PATCH_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    PATCH_CUDA(launch_q8_unpack(h->packed, h->slab_dev, h->meta_dev, h->plan.S, h->plan.KB, h->K, W, s));
+    PATCH_CUDA(launch_q8_unpack(h->packed, h->slab_dev, h->plan.S, h->plan.KB, h->K, W, s));
     PATCH_CUDA(cudaMemcpyAsync(w_scale, h->w_scale, sizeof(float) * h->N, cudaMemcpyDeviceToDevice, s));
     return PATCH_OK;
 }

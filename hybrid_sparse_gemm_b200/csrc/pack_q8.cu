@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(256) q8_pack_kernel(const Q8PackArgs a) {
     if (!(d & kSlabSparse)) {
         write_dense(a, s, b, base, true, bad, stray, pruned);
     } else {
-        uint8_t* meta = a.out + (uint64_t)a.meta[blockIdx.x] * 16;
+        uint8_t* meta = base + kSparseValBytes;
         // 512 items: row r, 32 columns from 32 L (8 groups, 16 kept codes)
         for (int q = threadIdx.x; q < 512; q += blockDim.x) {
             const int r = q >> 2, L = q & 3;
@@ -178,8 +178,7 @@ __global__ void __launch_bounds__(256) q8_pack_kernel(const Q8PackArgs a) {
 
 // Decode the per-strip records back to the masked codes, row-major N x K.
 __global__ void __launch_bounds__(256) q8_unpack_kernel(const uint8_t* __restrict__ packed,
-                                                        const uint32_t* __restrict__ slab,
-                                                        const uint32_t* __restrict__ meta_tab, int KB, int64_t K,
+                                                        const uint32_t* __restrict__ slab, int KB, int64_t K,
                                                         int8_t* __restrict__ W) {
     const int s = blockIdx.x / KB, b = blockIdx.x % KB;
     const uint32_t d = slab[blockIdx.x];
@@ -195,8 +194,7 @@ __global__ void __launch_bounds__(256) q8_unpack_kernel(const uint8_t* __restric
             // 16 columns: 4 groups, half of a 16-byte piece of kept codes
             __align__(8) int8_t kept[8];
             *reinterpret_cast<uint2*>(kept) = *reinterpret_cast<const uint2*>(base + sw64_off(r, L >> 1) + 8 * (L & 1));
-            const uint32_t code =
-                *reinterpret_cast<const uint16_t*>(packed + (uint64_t)meta_tab[blockIdx.x] * 16 + r * 16 + L * 2);
+            const uint32_t code = *reinterpret_cast<const uint16_t*>(base + kSparseValBytes + r * 16 + L * 2);
             *reinterpret_cast<uint4*>(c) = make_uint4(0, 0, 0, 0);
             for (int g = 0; g < 4; ++g) {
                 const uint32_t p = (code >> (4 * g)) & 15u;
@@ -220,9 +218,8 @@ cudaError_t launch_q8_pack(const Q8PackArgs& a, int S, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_q8_unpack(const uint8_t* packed, const uint32_t* slab, const uint32_t* meta, int S, int KB, int64_t K,
-                             int8_t* W, cudaStream_t st) {
-    q8_unpack_kernel<<<S * KB, 256, 0, st>>>(packed, slab, meta, KB, K, W);
+cudaError_t launch_q8_unpack(const uint8_t* packed, const uint32_t* slab, int S, int KB, int64_t K, int8_t* W, cudaStream_t st) {
+    q8_unpack_kernel<<<S * KB, 256, 0, st>>>(packed, slab, KB, K, W);
     return cudaGetLastError();
 }
 

@@ -1,15 +1,16 @@
 // 8-bit integer path: packed-format constants, kernel argument structs and
 // launch entry points shared by the host runtime.
 //
-// The packed format keeps the bf16 format's record sizes. A slab is a strip
-// (128 rows of W) times 128 columns: a dense slab is the 128 x 128 block of
-// codes, 128 bytes per row in the 128-byte-swizzled layout (16 KB); a 2:4
-// slab is 64 kept codes per row in the 64-byte-swizzled layout (8 KB) plus
-// its own 2 KB metadata block (one chunk per slab), 16 bytes per row: the
-// 4-bit code of group g of the slab (columns 4g .. 4g+3) at bit 4g of the
-// row's 128 bits. One tcgen05.cp.128x128b puts the block into four TMEM
-// columns, row r in lane r; each sparse MMA (K = 64) reads two of them. A
-// last slab of 64 columns (K % 128 == 64) is padded with zero codes.
+// A slab is a strip (128 rows of W) times 128 columns: a dense record is the
+// 128 x 128 block of codes, 128 bytes per row in the 128-byte-swizzled layout
+// (16 KB); a 2:4 record is 64 kept codes per row in the 64-byte-swizzled layout
+// (8 KB) followed by the slab's 2 KB of metadata, 16 bytes per row, so that one
+// copy brings both: the 4-bit code of group g of the slab (columns 4g .. 4g+3)
+// is at bit 4g of the row's 128 bits. One tcgen05.cp.128x128b puts the block
+// into four TMEM columns, row r in lane r; each sparse MMA (K = 64) reads two of
+// them. A last slab of 64 columns (K % 128 == 64) is padded with zero codes.
+// Records lie strip-major, then the dense images of 2:4 slabs whose partner
+// strip's slab is dense.
 #pragma once
 
 #include "kernels.cuh"
@@ -17,6 +18,10 @@
 namespace patch {
 
 constexpr int kQ8SlabK = 128;
+constexpr int kQ8SparseBytes = kSparseValBytes + kMetaBytes;
+__host__ __device__ inline uint32_t q8_record_bytes(uint32_t d) {
+    return (d & kSlabSparse) ? kQ8SparseBytes : kDenseSlabBytes;
+}
 
 // Output element types (match patch_dtype).
 constexpr int kBf16 = 0, kFp16 = 1, kFp32 = 2;
@@ -28,7 +33,6 @@ struct Q8PackArgs {
     int bitorder;             // 0 MSB first, 1 LSB first
     const uint8_t* flags;     // tile flags on the device, (N/R) x (K/C)
     const uint32_t* slab;     // per-strip slab table, S x KB
-    const uint32_t* meta;     // metadata block table, S x KB
     const uint32_t* gemm;     // CTA-pair slab table, S x KB
     float* w_scale;           // N channel scales (written for bf16 weights, read back by the pack)
     uint8_t* out;             // packed bytes
@@ -37,20 +41,18 @@ struct Q8PackArgs {
     unsigned long long* counters;  // [bad groups, stray zeros, pruned, bad scales]
 };
 cudaError_t launch_q8_pack(const Q8PackArgs& a, int S, cudaStream_t st);
-cudaError_t launch_q8_unpack(const uint8_t* packed, const uint32_t* slab, const uint32_t* meta, int S, int KB, int64_t K,
-                             int8_t* W, cudaStream_t st);
+cudaError_t launch_q8_unpack(const uint8_t* packed, const uint32_t* slab, int S, int KB, int64_t K, int8_t* W, cudaStream_t st);
 
 // Tensor maps of G members: activation codes (per call), and the packed bytes
-// viewed as 128-byte rows with 128-, 64- and 16-row boxes.
+// viewed as 128-byte rows with boxes of a dense (128 rows) and a 2:4 record (80).
 template <int G>
 struct Q8Maps {
-    CUtensorMap x[G], a16[G], a8[G], e[G];
+    CUtensorMap x[G], a16[G], a10[G];
 };
 
 // Split-K kernel: one cluster of P CTAs per unit (strip, token tile).
 struct Q8Member {
     const uint32_t* slab;  // S x KB
-    const uint32_t* meta;  // S x KB
     const float* x_scale;  // M
     const float* w_scale;  // N
     void* Y;
@@ -73,6 +75,33 @@ template <int G>
 cudaError_t launch_q8_split(const Q8Maps<G>& maps, const Q8SplitArgs<G>& a, int bn, int y_type, int grid,
                             cudaStream_t st);
 cudaError_t q8_prepare_split();
+
+// Kernel on CTA pairs with two strips per CTA (many tokens). A work unit is
+// (member << 24) | quad * MB + token tile; the MB tiles share M's 32-token
+// granules, tile_gran each and one more for the first tile_extra.
+struct Q8WideMember {
+    const uint32_t* gemm;  // CTA-pair slab table, rows in pair-position order
+    const int* order;      // strips by pair position
+    const float* x_scale;
+    const float* w_scale;
+    void* Y;
+    int64_t ldy;
+    int S, KB;
+};
+template <int G>
+struct Q8WideArgs {
+    Q8WideMember m[G];
+    const int* work_off;   // per CTA pair: [work_off[c], work_off[c+1])
+    const int* work;
+    int* status;
+    int M, MB;
+    int tile_gran, tile_extra;
+    int x_rows;            // rows of the activation boxes: half the largest tile
+};
+constexpr int kQ8WideBN = 224;  // tokens per tile: kind::i8 on a CTA pair takes multiples of 32
+template <int G>
+cudaError_t launch_q8_wide(const Q8Maps<G>& maps, const Q8WideArgs<G>& a, int y_type, int clusters, cudaStream_t st);
+cudaError_t q8_prepare_wide(int* max_clusters);
 
 // Row operators: one row of 8-bit codes and one scale per token.
 enum RowMode { kRowQuantize = 0, kRowNorm = 1, kRowNormResidual = 2, kRowSiluMul = 3 };

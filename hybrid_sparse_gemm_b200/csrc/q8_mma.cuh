@@ -2,7 +2,7 @@
 // accumulators.
 #pragma once
 
-#include "common.cuh"
+#include "pair.cuh"
 
 namespace patch {
 
@@ -31,22 +31,51 @@ __device__ __forceinline__ void mma_sp_i8(uint32_t d_tmem, uint64_t adesc, uint6
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(e_tmem)
         : "memory");
 }
+__device__ __forceinline__ void mma2_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma2_sp_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t e_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.sp.cta_group::2.kind::i8 [%0], %1, %2, [%5], %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(e_tmem)
+        : "memory");
+}
 
-// One slab on a single CTA: 4 dense MMAs of K = 32, or 2 sparse ones of
-// K = 64, each with two metadata columns. Operands advance by 32 bytes of A
-// and 32 (dense) or 64 (2:4) bytes of B per MMA.
+// One slab, on one CTA or (PAIR) on the CTA pair: 4 dense MMAs of K = 32, or 2
+// sparse ones of K = 64, each with two metadata columns. Operands advance by 32
+// bytes of A and 32 (dense) or 64 (2:4) bytes of B per MMA.
+template <bool PAIR>
 __device__ __forceinline__ void issue_slab_i8(bool sparse, bool first, uint32_t a_addr, uint32_t b_addr, uint32_t d_tmem,
                                               uint32_t e_col, uint32_t idesc_d, uint32_t idesc_s) {
     if (sparse) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            mma_sp_i8(d_tmem, smem_desc(a_addr + i * 32, 16, 512, kLayoutSw64),
-                      smem_desc(b_addr + i * 64, 16, 1024, kLayoutSw128), idesc_s, e_col + 2 * i, !(first && i == 0));
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t ad = smem_desc(a_addr + i * 32, 16, 512, kLayoutSw64);
+            const uint64_t bd = smem_desc(b_addr + i * 64, 16, 1024, kLayoutSw128);
+            if (PAIR)
+                mma2_sp_i8(d_tmem, ad, bd, idesc_s, e_col + 2 * i, !(first && i == 0));
+            else
+                mma_sp_i8(d_tmem, ad, bd, idesc_s, e_col + 2 * i, !(first && i == 0));
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            mma_i8(d_tmem, smem_desc(a_addr + i * 32, 16, 1024, kLayoutSw128),
-                   smem_desc(b_addr + i * 32, 16, 1024, kLayoutSw128), idesc_d, !(first && i == 0));
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t ad = smem_desc(a_addr + i * 32, 16, 1024, kLayoutSw128);
+            const uint64_t bd = smem_desc(b_addr + i * 32, 16, 1024, kLayoutSw128);
+            if (PAIR)
+                mma2_i8(d_tmem, ad, bd, idesc_d, !(first && i == 0));
+            else
+                mma_i8(d_tmem, ad, bd, idesc_d, !(first && i == 0));
+        }
     }
 }
 

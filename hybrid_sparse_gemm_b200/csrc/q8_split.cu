@@ -27,7 +27,6 @@
 // waits are bounded.
 #include <cuda_fp16.h>
 
-#include "pair.cuh"
 #include "q8.cuh"
 #include "q8_mma.cuh"
 
@@ -36,7 +35,7 @@ namespace patch {
 namespace {
 
 constexpr int kThreads = 192;
-constexpr int kStageA = 18432;  // 16 KB dense, or 8 KB codes + 2 KB metadata
+constexpr int kStageA = 16384;  // a dense record, or a 2:4 one (10 KB)
 
 template <int BN, int STAGES, int CTAS>
 struct Cfg {
@@ -101,17 +100,10 @@ __global__ void __launch_bounds__(kThreads, CTAS)
 
     // the CTA's slab records, fetched while the barriers are set up
     const uint32_t* drow = L.slab + (size_t)s * L.KB + b0;
-    const uint32_t* mrow = L.meta + (size_t)s * L.KB + b0;
-    uint32_t d_now = 0, m_now = 0, d_next = 0, m_next = 0;
+    uint32_t d_now = 0, d_next = 0;
     if (warp == 0) {
-        if (lane < nb) {
-            d_now = drow[lane];
-            m_now = mrow[lane];
-        }
-        if (32 + lane < nb) {
-            d_next = drow[32 + lane];
-            m_next = mrow[32 + lane];
-        }
+        if (lane < nb) d_now = drow[lane];
+        if (32 + lane < nb) d_next = drow[32 + lane];
     }
     if (threadIdx.x == 64) {
         for (int i = 0; i < STAGES; ++i) {
@@ -139,16 +131,14 @@ __global__ void __launch_bounds__(kThreads, CTAS)
     if (warp == 0) {
         // ---------------- producer ----------------
         const uint64_t pol_w = policy_evict_first();
-        auto load_w = [&](int i, uint32_t d, uint32_t m) {
+        auto load_w = [&](int i, uint32_t d) {
             const int st = i % STAGES;
             uint8_t* dst = smem + st * C::kStage;
             const bool sp = d & kSlabSparse;
             kind[st] = sp;
-            mbar_arrive_expect_tx(&full[st], (sp ? kSparseValBytes + kMetaBytes : kDenseSlabBytes) +
-                                                 (uint32_t)a.n_tok * 128u);
-            tma_load_2d_hint(dst, sp ? &maps.a8[l] : &maps.a16[l], &full[st], 0, (int)(slab_offset_bytes(d) >> 7),
+            mbar_arrive_expect_tx(&full[st], q8_record_bytes(d) + (uint32_t)a.n_tok * 128u);
+            tma_load_2d_hint(dst, sp ? &maps.a10[l] : &maps.a16[l], &full[st], 0, (int)(slab_offset_bytes(d) >> 7),
                              pol_w);
-            if (sp) tma_load_2d_hint(dst + kSparseValBytes, &maps.e[l], &full[st], 0, (int)(m >> 3), pol_w);
         };
         auto load_x = [&](int i) {
             const int st = i % STAGES;
@@ -156,8 +146,8 @@ __global__ void __launch_bounds__(kThreads, CTAS)
         };
         const int ahead = min(STAGES, nb);
         for (int i = 0; i < ahead; ++i) {
-            const uint32_t d = __shfl_sync(0xffffffffu, d_now, i), m = __shfl_sync(0xffffffffu, m_now, i);
-            if (lane == 0) load_w(i, d, m);
+            const uint32_t d = __shfl_sync(0xffffffffu, d_now, i);
+            if (lane == 0) load_w(i, d);
         }
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if (lane == 0)
@@ -167,20 +157,16 @@ __global__ void __launch_bounds__(kThreads, CTAS)
         for (; i < nb; ++i) {
             if (i % 32 == 0) {
                 d_now = d_next;
-                m_now = m_next;
-                if (i + 32 + lane < nb) {
-                    d_next = drow[i + 32 + lane];
-                    m_next = mrow[i + 32 + lane];
-                }
+                if (i + 32 + lane < nb) d_next = drow[i + 32 + lane];
             }
-            const uint32_t d = __shfl_sync(0xffffffffu, d_now, i % 32), m = __shfl_sync(0xffffffffu, m_now, i % 32);
+            const uint32_t d = __shfl_sync(0xffffffffu, d_now, i % 32);
             const bool ok = mbar_wait(&empty[i % STAGES], (uint32_t)((i / STAGES) & 1) ^ 1u, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) raise();
                 break;
             }
             if (lane == 0) {
-                load_w(i, d, m);
+                load_w(i, d);
                 load_x(i);
             }
             __syncwarp();
@@ -209,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, CTAS)
                 const uint32_t a_addr = smem_u32(smem + st * C::kStage);
                 const bool sp = kind[st];
                 if (sp) tc_cp_128x128b(e_col, smem_desc(a_addr + kSparseValBytes, 16, 128, kLayoutNone));
-                issue_slab_i8(sp, i == 0, a_addr, a_addr + kStageA, tmem_base, e_col, idesc_d, idesc_s);
+                issue_slab_i8<false>(sp, i == 0, a_addr, a_addr + kStageA, tmem_base, e_col, idesc_d, idesc_s);
                 tc_commit(&empty[st]);
             }
             // after a timeout this still covers the MMAs that were issued
@@ -301,7 +287,7 @@ cudaError_t launch(const Q8Maps<G>& maps, const Q8SplitArgs<G>& a, int grid, cud
 }
 
 // BN tokens per unit; stages and resident CTAs share the SM's shared memory.
-#define Q8_SPLIT_CONFIGS(X) X(16, 5, 2) X(64, 4, 2) X(128, 3, 2)
+#define Q8_SPLIT_CONFIGS(X) X(16, 6, 2) X(64, 4, 2) X(128, 3, 2)
 
 template <int BN, int STAGES, int CTAS>
 cudaError_t prepare_all() {

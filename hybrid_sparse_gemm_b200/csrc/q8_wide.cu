@@ -1,0 +1,407 @@
+// Hybrid dense / 2:4 product in 8-bit integers on CTA pairs with two strips per
+// CTA, for many tokens:
+// Y[m,n] = (sum_k Xq[m,k] * (Wq (.) Mask)[n,k]) * x_scale[m] * w_scale[n].
+//
+// The arrangement of the bf16 kernel for large launches (PATCH abstract,
+// "PATCH: Learnable Tile-level Hybrid Sparsity for LLMs", dense slabs on
+// tcgen05.mma, 2:4 slabs on tcgen05.mma.sp) with kind::i8. A cluster of two
+// CTAs owns a strip quad (pair positions 4c .. 4c+3) and a tile of up to 224
+// tokens. Every 128-column slab issues two 256-row MMAs (cta_group::2), one per
+// strip pair, so that each activation byte from L2 serves 512 weight rows: per
+// slab and CTA 20 KB of 2:4 records and 14 KB of activations feed 448 cycles of
+// the tensor pipe, 76 bytes a cycle, a little above the 68 that one SM was
+// measured to draw from L2. What feeds the pipe therefore decides the rate:
+// stages lie in a ring sized by their records (six 2:4 stages in flight), a
+// record and its metadata come in one copy, four warps issue copies and two
+// threads issue MMAs.
+//
+// TMEM: accumulators in columns [0, 224) and [256, 480), metadata of strip pair
+// 0 at 224 and of pair 1 at 232. All waits are bounded.
+#include <cuda_fp16.h>
+
+#include "q8.cuh"
+#include "q8_mma.cuh"
+
+namespace patch {
+
+namespace {
+
+constexpr int kProducers = 4;                   // TMA-issuing warps (stages dealt round robin)
+constexpr int kMmaWarp = kProducers;            // MMA issuers (leader CTA), one per strip pair;
+constexpr int kMmaWarps = 2;                    // the first also owns TMEM
+constexpr int kEpiWarp0 = kMmaWarp + kMmaWarps;
+constexpr int kEpiWarps = 16;                   // per accumulator, two warps per TMEM lane quarter
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kBN = kQ8WideBN;
+constexpr int kStageX = kBN / 2 * 128;          // 14 KB of activations per slab and CTA
+constexpr int kQ = 8;                           // per-stage barriers: more than the stages that fit in the ring
+constexpr int kMinStage = 2 * kQ8SparseBytes + kStageX;
+// Each producer warp keeps the slab records of its tile's two strips in shared
+// memory; weights with more slabs read them from global memory.
+constexpr int kTabKB = 256;                     // K up to 32768
+constexpr int kSmemTab = kProducers * 2 * kTabKB * 4;
+constexpr int kRing = (232448 - kSmemTab - 1024 - 512) / 1024 * 1024;
+constexpr int kSmemBytes = kRing + kSmemTab + 1024 + 512;
+static_assert(kStageX % 1024 == 0 && kQ8SparseBytes % 1024 == 0, "every record starts 1024-byte aligned");
+static_assert(kRing / kMinStage + 2 <= kQ, "stages in flight stay within the barrier window");
+constexpr int kAcc1 = 256;                      // first column of accumulator 1
+constexpr int kECol0 = kBN;                     // metadata columns of strip pair 0
+constexpr int kECol1 = kBN + 8;                 // ... and of strip pair 1
+constexpr int kTmemCols = 512;
+static_assert(kECol1 + 4 <= kAcc1, "metadata columns fit between the accumulators");
+
+template <class A>
+__device__ __forceinline__ int tile_start(const A& a, int j) {
+    return 32 * (j * a.tile_gran + min(j, a.tile_extra));
+}
+template <class A>
+__device__ __forceinline__ int tile_tokens(const A& a, int j) {
+    return 32 * (a.tile_gran + (j < a.tile_extra ? 1 : 0));
+}
+
+// What the MMA issuers need of a stage, written by the leader CTA's producer
+// that loads it, before the stage's loads are counted on its full barrier:
+// ring offset, record bytes of strip pair 0 | pair 1 << 16, and flags: bit 0
+// pair 0 is 2:4, bit 1 pair 1 is 2:4, bit 2 first stage of the tile, bit 3 last.
+struct StageDesc {
+    uint32_t off, bytes, flags;
+};
+
+// Stages are placed one after another in a ring of kRing bytes; a stage that
+// does not fit before the end starts again at 0. `pos` counts bytes placed so
+// far (including skipped ends); returns the ring offset of this stage.
+struct Ring {
+    uint32_t pos = 0, off = 0;
+    __device__ __forceinline__ uint32_t place(uint32_t size) {
+        if (off + size > (uint32_t)kRing) {
+            pos += (uint32_t)kRing - off;
+            off = 0;
+        }
+        const uint32_t at = off;
+        pos += size;
+        off += size;
+        return at;
+    }
+};
+
+// Two rows (lanes 2i and 2i+1) of one token as a pair.
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
+}
+__device__ __forceinline__ void store2(__half* p, float x, float y) {
+    *reinterpret_cast<__half2*>(p) = __floats2half2_rn(x, y);
+}
+__device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+
+template <int G, class T>
+__global__ void __launch_bounds__(kThreads, 1)
+    q8_wide_kernel(const __grid_constant__ Q8Maps<G> maps, const __grid_constant__ Q8WideArgs<G> a) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    uint32_t* tabs = reinterpret_cast<uint32_t*>(smem + kRing);  // [warp][2][kTabKB]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kRing + kSmemTab);
+    uint64_t* full = bars;                       // [kQ] leader: both CTAs' bytes of stage g (at g % kQ)
+    uint64_t* empty = full + kQ;                 // [kQ] every CTA: stage g consumed by both issuers
+    uint64_t* acc_full = empty + kQ;             // [2] both CTAs: accumulator h ready
+    uint64_t* acc_empty = acc_full + 2;          // [2] leader: the 16 epilogue warps of accumulator h drained it
+    uint64_t* drain = acc_empty + 2;             // [2]
+    StageDesc* sdesc = reinterpret_cast<StageDesc*>(drain + 2);  // [kQ] leader: stage g at g % kQ
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sdesc + kQ);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t pr = cluster_rank();          // CTA within the pair (0 = leader)
+    const int cl = blockIdx.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kQ; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kMmaWarps);
+        }
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(&acc_full[h], 1);
+            mbar_init(&acc_empty[h], kEpiWarps);  // its 8 epilogue warps in each of the 2 CTAs
+            mbar_init(&drain[h], 1);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc2(tmem_slot, kTmemCols);
+        tmem_relinquish2();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // barriers of both CTAs initialised before any remote use
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    auto raise = [&]() {
+        *abort_flag = 1;
+        atomicCAS(a.status, 0, kStatusTimeout);
+    };
+    // Pair position of the strip this CTA loads for strip pair h of quad c.
+    // Missing positions fall back to one whose partner relation is kept, so
+    // both halves of every MMA stay one kind.
+    auto pos_of = [&](int S, int c, int h) {
+        int pos = 4 * c + 2 * h + (int)pr;
+        if (pos >= S) pos = 4 * c + 2 * h;
+        if (pos >= S) pos = 4 * c + (int)pr;
+        if (pos >= S) pos = 4 * c;
+        return pos;
+    };
+    // the set-up above may overlap the stream's previous kernel
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int w_begin = a.work_off[cl];
+    const int w_end = a.work_off[cl + 1];
+
+    if (warp < kProducers) {
+        // ---------------- producers (both CTAs) ----------------
+        // Every producer walks the whole stage sequence to place each stage
+        // in the ring; it loads the stages g with g % kProducers == me.
+        // Before loading, the stages that last used those ring bytes must
+        // have been consumed (in order, so waiting for the latest suffices).
+        const int me = warp;
+        Ring ring;
+        uint32_t hist[kQ];   // ring positions where the last kQ stages started
+        int g = 0;
+        int my_last = -1;    // sequence index of the last stage this producer loaded
+        bool ok = true;
+        // every strip quad of a member reads the same activation tiles, so
+        // they are kept in L2 over the weight records (each read by one wave
+        // of token tiles)
+        const uint64_t pol_x = policy_evict_last();
+        const uint32_t x_bytes = (uint32_t)a.x_rows * 128u;
+        for (int it = w_begin; it < w_end && ok; ++it) {
+            const int u = a.work[it];
+            const int l = G > 1 ? u >> kUnitShift : 0, lu = u & kUnitMask;
+            const Q8WideMember& L = a.m[l];
+            const int c = lu / a.MB, j = lu % a.MB, KB = L.KB;
+            const uint32_t* t0 = L.gemm + (size_t)pos_of(L.S, c, 0) * KB;
+            const uint32_t* t1 = L.gemm + (size_t)pos_of(L.S, c, 1) * KB;
+            if (KB <= kTabKB) {
+                uint32_t* tab = tabs + warp * 2 * kTabKB;
+                for (int i = lane; i < KB; i += 32) {
+                    tab[i] = t0[i];
+                    tab[kTabKB + i] = t1[i];
+                }
+                t0 = tab;
+                t1 = tab + kTabKB;
+                __syncwarp();
+            }
+            const int tok = tile_start(a, j) + (int)pr * (tile_tokens(a, j) >> 1);
+            for (int b = 0; lane == 0 && b < KB; ++b, ++g) {
+                const uint32_t d0 = t0[b], d1 = t1[b];
+                const uint32_t r0 = q8_record_bytes(d0), r1 = q8_record_bytes(d1);
+                const uint32_t size = r0 + r1 + (uint32_t)kStageX;
+                const uint32_t off = ring.place(size);
+                hist[g % kQ] = ring.pos - size;
+                if (g % kProducers != me) continue;
+                if (ring.pos > (uint32_t)kRing) {
+                    const uint32_t need = ring.pos - (uint32_t)kRing;
+                    int jl = -1;
+                    for (int jj = g - 1; jj >= 0 && jj > g - kQ; --jj)
+                        if (hist[jj % kQ] < need) {
+                            jl = jj;
+                            break;
+                        }
+                    if (jl >= 0 && !mbar_wait(&empty[jl % kQ], (uint32_t)((jl / kQ) & 1), abort_flag)) {
+                        raise();
+                        ok = false;
+                        break;
+                    }
+                }
+                const uint32_t bar = map_to_rank(smem_u32(&full[g % kQ]), 0);
+                if (pr == 0) {
+                    StageDesc sd;
+                    sd.off = off;
+                    sd.bytes = r0 | (r1 << 16);
+                    sd.flags = (d0 & kSlabSparse) | ((d1 & kSlabSparse) << 1) | (b == 0 ? 4u : 0u) |
+                               (b + 1 == KB ? 8u : 0u);
+                    sdesc[g % kQ] = sd;
+                    mbar_arrive_expect_tx(&full[g % kQ], 2u * (r0 + r1 + x_bytes));
+                }
+                const uint32_t dst = smem_u32(smem) + off;
+                tma_load_2d_pair(dst, (d0 & kSlabSparse) ? &maps.a10[l] : &maps.a16[l], bar, 0,
+                                 (int)(slab_offset_bytes(d0) >> 7));
+                tma_load_2d_pair(dst + r0, (d1 & kSlabSparse) ? &maps.a10[l] : &maps.a16[l], bar, 0,
+                                 (int)(slab_offset_bytes(d1) >> 7));
+                tma_load_2d_pair_hint(dst + r0 + r1, &maps.x[l], bar, b * kQ8SlabK, tok, pol_x);
+                my_last = g;
+            }
+            // the whole warp moves on to the next tile (or stops) with lane 0
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            __syncwarp();
+        }
+        if (pr == 0 && lane == 0) {
+            // Bounded wait for the loads of my stages among the last kQ of
+            // the sequence, whatever the abort flag says, so none lands
+            // after the cluster exits.
+            for (int gg = g - kQ; gg <= my_last; ++gg) {
+                if (gg < 0 || gg % kProducers != me) continue;
+                const uint64_t t0 = globaltimer();
+                while (!mbar_try_wait(&full[gg % kQ], (uint32_t)((gg / kQ) & 1)) &&
+                       globaltimer() - t0 < kWaitLimitNs) {
+                }
+            }
+        }
+    } else if (warp < kMmaWarp + kMmaWarps) {
+        if (lane == 0 && pr == 0) {
+            // ---------------- MMA issuers (leader CTA), one per strip pair ----------------
+            // Both read every stage; a stage's ring bytes are free once both
+            // have committed it.
+            const int h = warp - kMmaWarp;
+            const uint32_t d_tmem = tmem_base + (uint32_t)(h * kAcc1);
+            const uint32_t e_col = tmem_base + (uint32_t)(h ? kECol1 : kECol0);
+            const uint32_t ring0 = smem_u32(smem);
+            int g = 0, t = 0;
+            bool ok = true, any_mma = false;
+            for (int it = w_begin; it < w_end && ok; ++it, ++t) {
+                const int nt = tile_tokens(a, (a.work[it] & kUnitMask) % a.MB);
+                const uint32_t idesc_d = idesc_i8(256, nt, false);
+                const uint32_t idesc_s = idesc_i8(256, nt, true);
+                if (!mbar_wait(&acc_empty[h], (t & 1) ^ 1u, abort_flag)) {
+                    raise();
+                    break;
+                }
+                tc_fence_after();
+                for (bool last = false; !last; ++g) {
+                    if (!mbar_wait(&full[g % kQ], (uint32_t)((g / kQ) & 1), abort_flag)) {
+                        raise();
+                        ok = false;
+                        break;
+                    }
+                    const StageDesc sd = sdesc[g % kQ];
+                    const uint32_t r0 = sd.bytes & 0xFFFFu, r1 = sd.bytes >> 16;
+                    const bool sp = (sd.flags >> h) & 1u;
+                    last = (sd.flags & 8u) != 0;
+                    const uint32_t a_addr = ring0 + sd.off + (h ? r0 : 0u);
+                    if (sp) cp2_128x128b(e_col, smem_desc(a_addr + kSparseValBytes, 16, 128, kLayoutNone));
+                    issue_slab_i8<true>(sp, (sd.flags & 4u) != 0, a_addr, ring0 + sd.off + r0 + r1, d_tmem, e_col,
+                                        idesc_d, idesc_s);
+                    any_mma = true;
+                    commit2_mask(&empty[g % kQ], 3);
+                }
+                if (!ok) break;
+                commit2_mask(&acc_full[h], 3);
+            }
+            if (*abort_flag && any_mma) {
+                commit2_local(&drain[h]);
+                const uint64_t t0 = globaltimer();
+                while (!mbar_try_wait(&drain[h], 0) && globaltimer() - t0 < kWaitLimitNs) {
+                }
+            }
+        }
+    } else {
+        // ---------------- epilogue (16 warps, both CTAs) ----------------
+        const int h = (warp - kEpiWarp0) >> 3;         // accumulator (strip pair) this warp drains
+        const int ch = ((warp - kEpiWarp0) >> 2) & 1;  // this warp takes every other 32-token chunk
+        const int q = warp & 3;                        // TMEM lane quarter this warp may access
+        const bool odd = lane & 1;
+        int t = 0;
+        for (int it = w_begin; it < w_end; ++it, ++t) {
+            const int u = a.work[it];
+            const int l = G > 1 ? u >> kUnitShift : 0, lu = u & kUnitMask;
+            const Q8WideMember& L = a.m[l];
+            const int c = lu / a.MB, j = lu % a.MB;
+            const int pos = 4 * c + 2 * h + (int)pr;   // pair position of this CTA's strip
+            const bool store = pos < L.S;
+            // lanes 2i and 2i+1 hold rows 2i and 2i+1; each stores both rows of one token in two
+            const int row = (store ? L.order[pos] : 0) * kStrip + q * 32 + (lane & ~1);
+            const float sw0 = L.w_scale[row], sw1 = L.w_scale[row + 1];
+            const int nt = tile_tokens(a, j), tok0 = tile_start(a, j);
+            const int64_t ldy = L.ldy;
+            T* y = static_cast<T*>(L.Y) + (int64_t)(tok0 + odd) * ldy + row;
+            const float* sx = L.x_scale + tok0 + odd;
+            const int mrem = a.M - tok0 - odd;         // tokens from this lane's first that exist
+            if (!mbar_wait(&acc_full[h], t & 1, abort_flag)) {
+                if (lane == 0) raise();
+                break;
+            }
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * kAcc1);
+            if (store) {
+#pragma unroll 1
+                for (int c0 = 32 * ch; c0 < nt; c0 += 64) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(taddr + c0, v);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int cc = 0; cc < 32; cc += 2) {
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[cc] : v[cc + 1], 1);
+                        if (c0 + cc < mrem) {
+                            const float s = sx[c0 + cc];
+                            const float y0 = (float)(int)(odd ? got : v[cc]) * s * sw0;
+                            const float y1 = (float)(int)(odd ? v[cc + 1] : got) * s * sw1;
+                            store2(y + (int64_t)(c0 + cc) * ldy, y0, y1);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) remote_arrive(map_to_rank(smem_u32(&acc_empty[h]), 0));
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // no CTA leaves while the other may still signal it
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc2(tmem_base, kTmemCols);
+    }
+}
+
+cudaLaunchConfig_t config(int clusters, cudaLaunchAttribute* attr, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * clusters, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+template <int G, class T>
+cudaError_t prepare() {
+    return cudaFuncSetAttribute(q8_wide_kernel<G, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+}
+
+}  // namespace
+
+cudaError_t q8_prepare_wide(int* max_clusters) {
+    cudaError_t e = prepare<1, __nv_bfloat16>();
+    if (e == cudaSuccess) e = prepare<1, __half>();
+    if (e == cudaSuccess) e = prepare<1, float>();
+    if (e == cudaSuccess) e = prepare<kMaxGroup, __nv_bfloat16>();
+    if (e == cudaSuccess) e = prepare<kMaxGroup, __half>();
+    if (e == cudaSuccess) e = prepare<kMaxGroup, float>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = config(1, attr, nullptr);
+    return cudaOccupancyMaxActiveClusters(max_clusters, q8_wide_kernel<1, __nv_bfloat16>, &cfg);
+}
+
+template <int G>
+cudaError_t launch_q8_wide(const Q8Maps<G>& maps, const Q8WideArgs<G>& a, int y_type, int clusters, cudaStream_t st) {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = config(clusters, attr, st);
+    return y_type == kBf16   ? cudaLaunchKernelEx(&cfg, q8_wide_kernel<G, __nv_bfloat16>, maps, a)
+           : y_type == kFp16 ? cudaLaunchKernelEx(&cfg, q8_wide_kernel<G, __half>, maps, a)
+                             : cudaLaunchKernelEx(&cfg, q8_wide_kernel<G, float>, maps, a);
+}
+template cudaError_t launch_q8_wide<1>(const Q8Maps<1>&, const Q8WideArgs<1>&, int, int, cudaStream_t);
+template cudaError_t launch_q8_wide<kMaxGroup>(const Q8Maps<kMaxGroup>&, const Q8WideArgs<kMaxGroup>&, int, int,
+                                               cudaStream_t);
+
+}  // namespace patch

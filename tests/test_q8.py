@@ -67,7 +67,7 @@ def assert_product(y, want):
 
 
 def paths(hsg, M):
-    return [hsg.PATH_AUTO, hsg.PATH_GEMM_SINGLE]
+    return [hsg.PATH_AUTO, hsg.PATH_GEMM_SINGLE, hsg.PATH_GEMM_WIDE] + ([hsg.PATH_GEMV] if M <= 64 else [])
 
 
 # --------------------------------------------------------------- packing ---
