@@ -40,8 +40,10 @@ constexpr int kMinStage = 2 * kQ8SparseBytes + kStageX;
 // memory; weights with more slabs read them from global memory.
 constexpr int kTabKB = 256;                     // K up to 32768
 constexpr int kSmemTab = kProducers * 2 * kTabKB * 4;
-constexpr int kRing = (232448 - kSmemTab - 1024 - 512) / 1024 * 1024;
-constexpr int kSmemBytes = kRing + kSmemTab + 1024 + 512;
+constexpr int kEpiCols = kBN / 2;               // columns of an epilogue warp
+constexpr int kSmemScales = kEpiWarps * kEpiCols * 4;
+constexpr int kRing = (232448 - kSmemTab - kSmemScales - 1024 - 512) / 1024 * 1024;
+constexpr int kSmemBytes = kRing + kSmemTab + kSmemScales + 1024 + 512;
 static_assert(kStageX % 1024 == 0 && kQ8SparseBytes % 1024 == 0, "every record starts 1024-byte aligned");
 static_assert(kRing / kMinStage + 2 <= kQ, "stages in flight stay within the barrier window");
 constexpr int kAcc1 = 256;                      // first column of accumulator 1
@@ -84,14 +86,15 @@ struct Ring {
     }
 };
 
-// Two rows (lanes 2i and 2i+1) of one token as a pair.
-__device__ __forceinline__ void store2(__nv_bfloat16* p, float x, float y) {
-    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
+// Two numbers as a pair of 16-bit ones, the first in the low half.
+__device__ __forceinline__ uint32_t pack2(float x, float y, __nv_bfloat16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ void store2(__half* p, float x, float y) {
-    *reinterpret_cast<__half2*>(p) = __floats2half2_rn(x, y);
+__device__ __forceinline__ uint32_t pack2(float x, float y, __half) {
+    const __half2 v = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ void store2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
 
 template <int G, class T>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -100,7 +103,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     uint32_t* tabs = reinterpret_cast<uint32_t*>(smem + kRing);  // [warp][2][kTabKB]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kRing + kSmemTab);
+    float* scales = reinterpret_cast<float*>(smem + kRing + kSmemTab);  // [epilogue warp][kEpiCols]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kRing + kSmemTab + kSmemScales);
     uint64_t* full = bars;                       // [kQ] leader: both CTAs' bytes of stage g (at g % kQ)
     uint64_t* empty = full + kQ;                 // [kQ] every CTA: stage g consumed by both issuers
     uint64_t* acc_full = empty + kQ;             // [2] both CTAs: accumulator h ready
@@ -296,10 +300,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------- epilogue (16 warps, both CTAs) ----------------
-        const int h = (warp - kEpiWarp0) >> 3;         // accumulator (strip pair) this warp drains
-        const int ch = ((warp - kEpiWarp0) >> 2) & 1;  // this warp takes every other 32-token chunk
-        const int q = warp & 3;                        // TMEM lane quarter this warp may access
-        const bool odd = lane & 1;
+        const int w = warp - kEpiWarp0;
+        const int h = w >> 3;                    // accumulator (strip pair) this warp drains
+        const int q = warp & 3;                  // TMEM lane quarter this warp may access
+        float* sx = scales + w * kEpiCols;       // the token scales of this warp's columns
         int t = 0;
         for (int it = w_begin; it < w_end; ++it, ++t) {
             const int u = a.work[it];
@@ -308,41 +312,75 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c = lu / a.MB, j = lu % a.MB;
             const int pos = 4 * c + 2 * h + (int)pr;   // pair position of this CTA's strip
             const bool store = pos < L.S;
-            // lanes 2i and 2i+1 hold rows 2i and 2i+1; each stores both rows of one token in two
-            const int row = (store ? L.order[pos] : 0) * kStrip + q * 32 + (lane & ~1);
-            const float sw0 = L.w_scale[row], sw1 = L.w_scale[row + 1];
-            const int nt = tile_tokens(a, j), tok0 = tile_start(a, j);
+            const int row = (store ? L.order[pos] : 0) * kStrip + q * 32 + lane;
+            const float sw = L.w_scale[row];
+            const int cols = tile_tokens(a, j) / 2;    // half of the tile's columns, the first or the second
+            const int tok0 = tile_start(a, j) + ((w >> 2) & 1) * cols;
             const int64_t ldy = L.ldy;
-            T* y = static_cast<T*>(L.Y) + (int64_t)(tok0 + odd) * ldy + row;
-            const float* sx = L.x_scale + tok0 + odd;
-            const int mrem = a.M - tok0 - odd;         // tokens from this lane's first that exist
+            for (int i = lane; i < cols; i += 32) sx[i] = tok0 + i < a.M ? L.x_scale[tok0 + i] : 0.f;
+            __syncwarp();
             if (!mbar_wait(&acc_full[h], t & 1, abort_flag)) {
                 if (lane == 0) raise();
                 break;
             }
             tc_fence_after();
-            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * kAcc1);
-            if (store) {
-#pragma unroll 1
-                for (int c0 = 32 * ch; c0 < nt; c0 += 64) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(taddr + c0, v);
+            const uint32_t taddr =
+                tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * kAcc1 + ((w >> 2) & 1) * cols);
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) remote_arrive(map_to_rank(smem_u32(&acc_empty[h]), 0));
+            };
+            if constexpr (sizeof(T) == 2) {
+                // The whole half-tile is scaled, rounded and packed in registers
+                // (two tokens each) and the accumulator handed back before the
+                // first store: all CTAs finish a tile at about the same time,
+                // and the burst of stores then overlaps the next tile's MMAs.
+                uint32_t p[kEpiCols / 16][8];
+#pragma unroll
+                for (int k = 0; k < kEpiCols / 16; ++k) {
+                    if (16 * k >= cols) break;
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(taddr + 16 * k, v);
                     tc_wait_ld();
 #pragma unroll
-                    for (int cc = 0; cc < 32; cc += 2) {
-                        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[cc] : v[cc + 1], 1);
-                        if (c0 + cc < mrem) {
-                            const float s = sx[c0 + cc];
-                            const float y0 = (float)(int)(odd ? got : v[cc]) * s * sw0;
-                            const float y1 = (float)(int)(odd ? v[cc + 1] : got) * s * sw1;
-                            store2(y + (int64_t)(c0 + cc) * ldy, y0, y1);
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 f = *reinterpret_cast<const float4*>(sx + 16 * k + 4 * e);
+                        p[k][2 * e] = pack2((float)(int)v[4 * e] * f.x * sw, (float)(int)v[4 * e + 1] * f.y * sw, T());
+                        p[k][2 * e + 1] =
+                            pack2((float)(int)v[4 * e + 2] * f.z * sw, (float)(int)v[4 * e + 3] * f.w * sw, T());
                     }
                 }
+                release();
+                if (!store) continue;
+                // lanes 2i and 2i+1 hold rows 2i and 2i+1 of tokens 2e and 2e+1;
+                // after one swap each stores both rows of one token
+                const bool odd = lane & 1;
+                T* y = static_cast<T*>(L.Y) + (int64_t)(tok0 + odd) * ldy + (row & ~1);
+                const int mrem = a.M - tok0 - odd;
+#pragma unroll
+                for (int k = 0; k < kEpiCols / 16; ++k) {
+                    if (16 * k >= cols) break;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, p[k][e], 1);
+                        const uint32_t two = __byte_perm(p[k][e], got, odd ? 0x3276 : 0x5410);
+                        if (16 * k + 2 * e < mrem) *reinterpret_cast<uint32_t*>(y + (16 * k + 2 * e) * ldy) = two;
+                    }
+                }
+            } else {
+                T* y = static_cast<T*>(L.Y) + (int64_t)tok0 * ldy + row;
+#pragma unroll 1
+                for (int k = 0; k < cols && store; k += 16) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(taddr + k, v);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (tok0 + k + e < a.M) y[(k + e) * ldy] = (float)(int)v[e] * sx[k + e] * sw;
+                }
+                release();
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) remote_arrive(map_to_rank(smem_u32(&acc_empty[h]), 0));
         }
     }
 
