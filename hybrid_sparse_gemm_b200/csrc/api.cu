@@ -285,6 +285,21 @@ void build_plan(Plan& p, int64_t N, int64_t K, int R, int C, const uint8_t* flag
         }
     auto is_sp = [&](int s, int b) { return sp[(size_t)s * p.KB + b] != 0; };
     p.order = pair_order(sp, p.S, p.KB);
+    if (q8) {
+        // the 8-bit kernel takes pairs in the order of falling cost
+        std::vector<std::pair<int, int>> by;  // (2:4 slabs of the pair, its position)
+        for (int i = 0; i + 1 < p.S; i += 2) {
+            int n = 0;
+            for (int b = 0; b < p.KB; ++b) n += is_sp(p.order[i], b) && is_sp(p.order[i + 1], b);
+            by.push_back({n, i});
+        }
+        std::sort(by.begin(), by.end());
+        const std::vector<int> was = p.order;
+        for (size_t i = 0; i < by.size(); ++i) {
+            p.order[2 * i] = was[by[i].second];
+            p.order[2 * i + 1] = was[by[i].second + 1];
+        }
+    }
     std::vector<int> partner_of(p.S);
     for (int q = 0; q < p.S; ++q) partner_of[p.order[q]] = (q ^ 1) < p.S ? p.order[q ^ 1] : p.order[q];
     auto pair_sp = [&](int s, int b) { return is_sp(s, b) && is_sp(partner_of[s], b); };
@@ -658,8 +673,6 @@ patch_status get_decode_ws(patch_group g, cudaStream_t st, int bn, const DecodeW
 // MMAs, 4 CTA pair with two strips per CTA, 5 decode with 64-token MMAs):
 // tokens per tile,
 // activation rows per TMA box, weight rows of a work unit, persistent slots.
-// The 8-bit kernel that runs a schedule: CTA pair with two strips per CTA.
-constexpr int kQ8Wide = 14;
 constexpr int64_t kQ8MaxK = 131008;  // K * 128 * 128 stays below 2^31
 
 int kernel_bn(int kernel) {
@@ -677,7 +690,6 @@ int64_t kernel_rows(const Plan& p, int kernel) {
     return kernel == 0 ? (int64_t)p.strip_cost.size() : kernel == 1 ? pairs : (pairs + 1) / 2;
 }
 int kernel_slots(const DeviceInfo& d, int kernel) {
-    if (kernel == kQ8Wide) return d.q8_wide_clusters;
     return kernel == 1   ? d.pair_clusters
            : kernel == 4 ? d.wide_clusters
            : kernel == 2 ? kDecodeCtasPerSm * d.sms
@@ -691,8 +703,6 @@ void lpt_schedule(patch_group g, int kernel, int mb, std::vector<int>& off, std:
         int id;
     };
     std::vector<Unit> units;
-    const int slots = kernel_slots(g->dev, kernel);
-    if (kernel == kQ8Wide) kernel = 4;
     for (int l = 0; l < g->n; ++l) {
         const Plan& p = g->h[l]->plan;
         if (kernel == 0 || kernel == 1) {
@@ -714,7 +724,7 @@ void lpt_schedule(patch_group g, int kernel, int mb, std::vector<int>& off, std:
         }
     }
     std::stable_sort(units.begin(), units.end(), [](const Unit& x, const Unit& y) { return x.cost > y.cost; });
-    const int grid = std::max(1, std::min(slots, (int)units.size()));
+    const int grid = std::max(1, std::min(kernel_slots(g->dev, kernel), (int)units.size()));
     using Item = std::pair<double, int>;
     std::priority_queue<Item, std::vector<Item>, std::greater<Item>> pq;
     for (int c = 0; c < grid; ++c) pq.push({0.0, c});
@@ -1029,15 +1039,20 @@ patch_status run_q8_wide(patch_group g, const Q8Call& c, cudaStream_t st) {
     a.tile_extra = (int)(gran % mb);
     a.x_rows = 16 * (a.tile_gran + (a.tile_extra ? 1 : 0));
     a.status = g->status_dev;
+    a.n = g->n;
+    // members of long K first, so that the last wave is made of short units
+    int by_cost[kMaxGroup];
+    for (int l = 0; l < g->n; ++l) by_cost[l] = l;
+    std::stable_sort(by_cost, by_cost + g->n, [&](int x, int y) { return g->h[x]->plan.KB > g->h[y]->plan.KB; });
+    int64_t units = 0;
     patch_status s;
-    for (int l = 0; l < g->n; ++l) {
+    for (int i = 0; i < g->n; ++i) {
+        const int l = by_cost[i];
         patch_handle h = g->h[l];
-        if ((h->plan.S + 3) / 4 * mb > kUnitMask)
-            return fail(PATCH_ERR_SHAPE, "M=%lld gives more than %d output tiles", (long long)c.M, kUnitMask);
-        if ((s = encode_codes(&maps.x[l], c.X[l], h->K, c.M, c.pitch_x(l, h->K), a.x_rows)) != PATCH_OK) return s;
-        maps.a16[l] = h->tm_a16;
-        maps.a10[l] = h->tm_a10;
-        Q8WideMember& m = a.m[l];
+        if ((s = encode_codes(&maps.x[i], c.X[l], h->K, c.M, c.pitch_x(l, h->K), a.x_rows)) != PATCH_OK) return s;
+        maps.a16[i] = h->tm_a16;
+        maps.a10[i] = h->tm_a10;
+        Q8WideMember& m = a.m[i];
         m.gemm = h->pgemm_dev;
         m.order = h->order_dev;
         m.x_scale = c.x_scale[l];
@@ -1046,12 +1061,14 @@ patch_status run_q8_wide(patch_group g, const Q8Call& c, cudaStream_t st) {
         m.ldy = c.pitch_y(l, h->N);
         m.S = h->plan.S;
         m.KB = h->plan.KB;
+        m.unit0 = (int)units;
+        units += (h->plan.S + 3) / 4 * mb;
+        if (units > INT32_MAX / 2)
+            return fail(PATCH_ERR_SHAPE, "M=%lld gives more than %d output tiles", (long long)c.M, INT32_MAX / 2);
     }
-    WorkList* wl = nullptr;
-    if ((s = get_worklist(g, kQ8Wide, (int)mb, st, &wl)) != PATCH_OK) return s;
-    a.work_off = wl->off;
-    a.work = wl->work;
-    const cudaError_t e = launch_q8_wide<G>(maps, a, c.y_type, wl->grid, st);
+    a.units = (int)units;
+    const int clusters = (int)std::min<int64_t>(units, g->dev.q8_wide_clusters);
+    const cudaError_t e = launch_q8_wide<G>(maps, a, c.y_type, clusters, st);
     if (e != cudaSuccess) return cuda_fail(e, "8-bit kernel launch");
     return PATCH_OK;
 }

@@ -77,8 +77,8 @@ cudaError_t launch_q8_split(const Q8Maps<G>& maps, const Q8SplitArgs<G>& a, int 
 cudaError_t q8_prepare_split();
 
 // Kernel on CTA pairs with two strips per CTA (many tokens). A work unit is
-// (member << 24) | quad * MB + token tile; the MB tiles share M's 32-token
-// granules, tile_gran each and one more for the first tile_extra.
+// (member, strip quad, token tile); the MB tiles share M's 32-token granules,
+// tile_gran each and one more for the first tile_extra.
 struct Q8WideMember {
     const uint32_t* gemm;  // CTA-pair slab table, rows in pair-position order
     const int* order;      // strips by pair position
@@ -87,13 +87,13 @@ struct Q8WideMember {
     void* Y;
     int64_t ldy;
     int S, KB;
+    int unit0;             // the member's first unit
 };
 template <int G>
 struct Q8WideArgs {
     Q8WideMember m[G];
-    const int* work_off;   // per CTA pair: [work_off[c], work_off[c+1])
-    const int* work;
     int* status;
+    int n, units;          // members, units of all of them
     int M, MB;
     int tile_gran, tile_extra;
     int x_rows;            // rows of the activation boxes: half the largest tile

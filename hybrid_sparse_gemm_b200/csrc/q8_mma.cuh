@@ -50,6 +50,14 @@ __device__ __forceinline__ void mma2_sp_i8(uint32_t d_tmem, uint64_t adesc, uint
         : "memory");
 }
 
+// 32 lanes x 8 columns of 32-bit.
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t* v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
 // One slab, on one CTA or (PAIR) on the CTA pair: 4 dense MMAs of K = 32, or 2
 // sparse ones of K = 64, each with two metadata columns. Operands advance by 32
 // bytes of A and 32 (dense) or 64 (2:4) bytes of B per MMA.

@@ -29,7 +29,7 @@ namespace {
 constexpr int kProducers = 4;                   // TMA-issuing warps (stages dealt round robin)
 constexpr int kMmaWarp = kProducers;            // MMA issuers (leader CTA), one per strip pair;
 constexpr int kMmaWarps = 2;                    // the first also owns TMEM
-constexpr int kEpiWarp0 = kMmaWarp + kMmaWarps;
+constexpr int kEpiWarp0 = 8;                    // (two warps idle: register splits go by warpgroup)
 constexpr int kEpiWarps = 16;                   // per accumulator, two warps per TMEM lane quarter
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kBN = kQ8WideBN;
@@ -46,6 +46,16 @@ constexpr int kRing = (232448 - kSmemTab - kSmemScales - 1024 - 512) / 1024 * 10
 constexpr int kSmemBytes = kRing + kSmemTab + kSmemScales + 1024 + 512;
 static_assert(kStageX % 1024 == 0 && kQ8SparseBytes % 1024 == 0, "every record starts 1024-byte aligned");
 static_assert(kRing / kMinStage + 2 <= kQ, "stages in flight stay within the barrier window");
+// A wait for stage j's phase by parity is right only once stage j - kQ is known
+// to be consumed. A producer that loads stage g waits for a j <= g - 4 (a ring of
+// at least four stages); its previous stage, g - kProducers, waited for one after
+// g - kProducers - kQ.
+static_assert(kProducers <= 4 && kRing / (2 * kDenseSlabBytes + kStageX) >= 4, "no wait is two phases ahead");
+// Registers: launched with 80 a thread (768 threads); the producers' warpgroup
+// gives up 24 of them and the issuers' 40, the four epilogue warpgroups take 16
+// more: 128 * (56 + 40 + 4 * 96) = 61440, what the block was launched with.
+constexpr int kRegsProduce = 56, kRegsIssue = 40, kRegsEpi = 96;
+static_assert(128 * (kRegsProduce + kRegsIssue + 4 * kRegsEpi) <= kThreads * 80, "the register split adds up");
 constexpr int kAcc1 = 256;                      // first column of accumulator 1
 constexpr int kECol0 = kBN;                     // metadata columns of strip pair 0
 constexpr int kECol1 = kBN + 8;                 // ... and of strip pair 1
@@ -155,14 +165,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (pos >= S) pos = 4 * c;
         return pos;
     };
-    // the set-up above may overlap the stream's previous kernel
+    // Unit u is (member, quad, token tile); pair cl takes units cl, cl + pairs, ...
+    // Units of one wave share their quads' weights in L2; quads and members come in
+    // the order of falling cost.
+    const int pairs = gridDim.x >> 1;
+    struct Unit {
+        int l, c, j;
+    };
+    auto unit_of = [&](int u) {
+        Unit x;
+        x.l = 0;
+        if (G > 1)
+            while (x.l + 1 < a.n && u >= a.m[x.l + 1].unit0) ++x.l;
+        u -= a.m[x.l].unit0;
+        x.c = u / a.MB;
+        x.j = u - x.c * a.MB;
+        return x;
+    };
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int w_begin = a.work_off[cl];
-    const int w_end = a.work_off[cl + 1];
 
     if (warp < kProducers) {
         // ---------------- producers (both CTAs) ----------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProduce));
         // Every producer walks the whole stage sequence to place each stage
         // in the ring; it loads the stages g with g % kProducers == me.
         // Before loading, the stages that last used those ring bytes must
@@ -178,11 +202,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // of token tiles)
         const uint64_t pol_x = policy_evict_last();
         const uint32_t x_bytes = (uint32_t)a.x_rows * 128u;
-        for (int it = w_begin; it < w_end && ok; ++it) {
-            const int u = a.work[it];
-            const int l = G > 1 ? u >> kUnitShift : 0, lu = u & kUnitMask;
+        // Until the ring is full for the first time only weights are loaded: they
+        // do not depend on the stream's previous kernel. Activations (at most two
+        // of this warp's stages are then without theirs) follow once it is done.
+        bool waited = false;
+        int n_pend = 0, pend_b[2], pend_l = 0, pend_tok = 0;
+        uint32_t pend_dst[2], pend_bar[2];
+        for (int u = cl; u < a.units && ok; u += pairs) {
+            const Unit un = unit_of(u);
+            const int l = un.l, c = un.c, j = un.j;
             const Q8WideMember& L = a.m[l];
-            const int c = lu / a.MB, j = lu % a.MB, KB = L.KB;
+            const int KB = L.KB;
             const uint32_t* t0 = L.gemm + (size_t)pos_of(L.S, c, 0) * KB;
             const uint32_t* t1 = L.gemm + (size_t)pos_of(L.S, c, 1) * KB;
             if (KB <= kTabKB) {
@@ -203,6 +233,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t off = ring.place(size);
                 hist[g % kQ] = ring.pos - size;
                 if (g % kProducers != me) continue;
+                if (!waited && (ring.pos > (uint32_t)kRing || u != cl || n_pend == 2)) {
+                    asm volatile("griddepcontrol.wait;" ::: "memory");
+                    waited = true;
+                    for (int i = 0; i < n_pend; ++i)
+                        tma_load_2d_pair_hint(pend_dst[i], &maps.x[pend_l], pend_bar[i], pend_b[i] * kQ8SlabK, pend_tok,
+                                              pol_x);
+                }
                 if (ring.pos > (uint32_t)kRing) {
                     const uint32_t need = ring.pos - (uint32_t)kRing;
                     int jl = -1;
@@ -232,12 +269,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  (int)(slab_offset_bytes(d0) >> 7));
                 tma_load_2d_pair(dst + r0, (d1 & kSlabSparse) ? &maps.a10[l] : &maps.a16[l], bar, 0,
                                  (int)(slab_offset_bytes(d1) >> 7));
-                tma_load_2d_pair_hint(dst + r0 + r1, &maps.x[l], bar, b * kQ8SlabK, tok, pol_x);
+                if (waited) {
+                    tma_load_2d_pair_hint(dst + r0 + r1, &maps.x[l], bar, b * kQ8SlabK, tok, pol_x);
+                } else {
+                    pend_dst[n_pend] = dst + r0 + r1;
+                    pend_bar[n_pend] = bar;
+                    pend_b[n_pend++] = b;
+                    pend_l = l;
+                    pend_tok = tok;
+                }
                 my_last = g;
             }
             // the whole warp moves on to the next tile (or stops) with lane 0
             ok = __shfl_sync(0xffffffffu, ok, 0);
             __syncwarp();
+        }
+        if (lane == 0 && !waited) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            for (int i = 0; i < n_pend; ++i)
+                tma_load_2d_pair_hint(pend_dst[i], &maps.x[pend_l], pend_bar[i], pend_b[i] * kQ8SlabK, pend_tok, pol_x);
         }
         if (pr == 0 && lane == 0) {
             // Bounded wait for the loads of my stages among the last kQ of
@@ -251,8 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp < kMmaWarp + kMmaWarps) {
-        if (lane == 0 && pr == 0) {
+    } else if (warp < kEpiWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+        if (lane == 0 && pr == 0 && warp < kMmaWarp + kMmaWarps) {
             // ---------------- MMA issuers (leader CTA), one per strip pair ----------------
             // Both read every stage; a stage's ring bytes are free once both
             // have committed it.
@@ -262,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t ring0 = smem_u32(smem);
             int g = 0, t = 0;
             bool ok = true, any_mma = false;
-            for (int it = w_begin; it < w_end && ok; ++it, ++t) {
-                const int nt = tile_tokens(a, (a.work[it] & kUnitMask) % a.MB);
+            for (int u = cl; u < a.units && ok; u += pairs, ++t) {
+                const int nt = tile_tokens(a, unit_of(u).j);
                 const uint32_t idesc_d = idesc_i8(256, nt, false);
                 const uint32_t idesc_s = idesc_i8(256, nt, true);
                 if (!mbar_wait(&acc_empty[h], (t & 1) ^ 1u, abort_flag)) {
@@ -300,16 +351,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------- epilogue (16 warps, both CTAs) ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         const int w = warp - kEpiWarp0;
         const int h = w >> 3;                    // accumulator (strip pair) this warp drains
         const int q = warp & 3;                  // TMEM lane quarter this warp may access
         float* sx = scales + w * kEpiCols;       // the token scales of this warp's columns
         int t = 0;
-        for (int it = w_begin; it < w_end; ++it, ++t) {
-            const int u = a.work[it];
-            const int l = G > 1 ? u >> kUnitShift : 0, lu = u & kUnitMask;
-            const Q8WideMember& L = a.m[l];
-            const int c = lu / a.MB, j = lu % a.MB;
+        for (int u = cl; u < a.units; u += pairs, ++t) {
+            const Unit un = unit_of(u);
+            const int c = un.c, j = un.j;
+            const Q8WideMember& L = a.m[un.l];
             const int pos = 4 * c + 2 * h + (int)pr;   // pair position of this CTA's strip
             const bool store = pos < L.S;
             const int row = (store ? L.order[pos] : 0) * kStrip + q * 32 + lane;
@@ -336,20 +388,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (two tokens each) and the accumulator handed back before the
                 // first store: all CTAs finish a tile at about the same time,
                 // and the burst of stores then overlaps the next tile's MMAs.
-                uint32_t p[kEpiCols / 16][8];
+                // Eight columns at a time, the next eight on their way.
+                uint32_t p[kEpiCols / 8][4], buf[2][8];
+                tmem_ld_32x32b_x8(taddr, buf[0]);
+                tc_wait_ld();
 #pragma unroll
-                for (int k = 0; k < kEpiCols / 16; ++k) {
-                    if (16 * k >= cols) break;
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(taddr + 16 * k, v);
-                    tc_wait_ld();
+                for (int k = 0; k < kEpiCols / 8; ++k) {
+                    if (8 * k >= cols) break;
+                    uint32_t* v = buf[k & 1];
+                    if (8 * (k + 1) < cols) tmem_ld_32x32b_x8(taddr + 8 * (k + 1), buf[(k + 1) & 1]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4 f = *reinterpret_cast<const float4*>(sx + 16 * k + 4 * e);
+                    for (int e = 0; e < 2; ++e) {
+                        const float4 f = *reinterpret_cast<const float4*>(sx + 8 * k + 4 * e);
                         p[k][2 * e] = pack2((float)(int)v[4 * e] * f.x * sw, (float)(int)v[4 * e + 1] * f.y * sw, T());
                         p[k][2 * e + 1] =
                             pack2((float)(int)v[4 * e + 2] * f.z * sw, (float)(int)v[4 * e + 3] * f.w * sw, T());
                     }
+                    tc_wait_ld();
                 }
                 release();
                 if (!store) continue;
@@ -359,13 +414,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 T* y = static_cast<T*>(L.Y) + (int64_t)(tok0 + odd) * ldy + (row & ~1);
                 const int mrem = a.M - tok0 - odd;
 #pragma unroll
-                for (int k = 0; k < kEpiCols / 16; ++k) {
-                    if (16 * k >= cols) break;
+                for (int k = 0; k < kEpiCols / 8; ++k) {
+                    if (8 * k >= cols) break;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         const uint32_t got = __shfl_xor_sync(0xffffffffu, p[k][e], 1);
                         const uint32_t two = __byte_perm(p[k][e], got, odd ? 0x3276 : 0x5410);
-                        if (16 * k + 2 * e < mrem) *reinterpret_cast<uint32_t*>(y + (16 * k + 2 * e) * ldy) = two;
+                        if (8 * k + 2 * e < mrem) *reinterpret_cast<uint32_t*>(y + (8 * k + 2 * e) * ldy) = two;
                     }
                 }
             } else {
