@@ -9,7 +9,17 @@
 // All sums are fp32. A row that holds a NaN or an infinity (or whose sum of
 // squares overflows) gets the scale NaN and zero codes, so that a product
 // over it is NaN instead of silently wrong.
+//
+// The kernels are bound by HBM for many rows and by latency for few. A row is
+// spread over as many threads as give each one or two groups of eight
+// elements; blocks are persistent, and every thread copies its groups of the
+// next rows into its own slots of shared memory (cp.async, no barrier), so that
+// loads stay in flight across the reductions without holding registers. Rows
+// that do not lie on 16-byte boundaries are taken in groups that do (the first
+// and the last one partial); what lies at another offset is shifted into place.
 #include <cuda_fp16.h>
+
+#include <atomic>
 
 #include "q8.cuh"
 
@@ -36,33 +46,93 @@ __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v
 template <>
 __device__ __forceinline__ float from_float(float v) { return v; }
 
-// VEC consecutive elements: 16-byte accesses for VEC = 8, single ones for VEC = 1.
-template <class T, int VEC>
-__device__ __forceinline__ void load(const T* p, float* v) {
-    if constexpr (VEC == 1) {
-        v[0] = to_float(*p);
-    } else {
-        constexpr int N = VEC * (int)sizeof(T) / 16;
-        uint4 raw[N];
+// Eight elements as they lie in memory.
+template <class T>
+struct Raw {
+    uint4 w[sizeof(T) / 2];
+};
+template <class T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p) {  // p on a 16-byte boundary
+    Raw<T> r;
 #pragma unroll
-        for (int i = 0; i < N; ++i) raw[i] = reinterpret_cast<const uint4*>(p)[i];
-        const T* e = reinterpret_cast<const T*>(raw);
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+    return r;
+}
+template <class T>
+__device__ __forceinline__ void unpack(const Raw<T>& r, float* v) {
+    const T* e = reinterpret_cast<const T*>(r.w);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = to_float(e[i]);
+    for (int i = 0; i < 8; ++i) v[i] = to_float(e[i]);
+}
+
+template <class T>
+__device__ __forceinline__ void store_raw(T* p, const float* v) {
+    Raw<T> r;
+    T* e = reinterpret_cast<T*>(r.w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = from_float<T>(v[i]);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
+}
+
+// Words w[0 .. N) shifted down by `bytes` (0..15, the same in a warp), from N + 4 words.
+template <int N>
+__device__ __forceinline__ void shift_down(uint32_t* w, int bytes) {
+    if (bytes & 8) {
+#pragma unroll
+        for (int i = 0; i < N + 2; ++i) w[i] = w[i + 2];
+    }
+    if (bytes & 4) {
+#pragma unroll
+        for (int i = 0; i < N + 1; ++i) w[i] = w[i + 1];
+    }
+    if (bytes & 3) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (bytes & 3));
     }
 }
-template <class T, int VEC>
-__device__ __forceinline__ void store(T* p, const float* v) {
-    if constexpr (VEC == 1) {
-        *p = from_float<T>(v[0]);
+
+// Elements [e, e + 8) of a row of K at any alignment; zeros outside the row. No
+// byte outside the row is read.
+template <class T>
+__device__ __forceinline__ void load_any(const T* row, int e, int K, float* v) {
+    const int off = (int)(reinterpret_cast<uintptr_t>(row + e) & 15u);
+    constexpr int kBytes = 8 * (int)sizeof(T);
+    const int64_t at = (int64_t)e * (int)sizeof(T) - off;  // from the row's start, of the boundary below
+    if (off == 0 && e >= 0 && e + 8 <= K) {
+        unpack(load_raw(row + e), v);
+    } else if (at >= 0 && at + kBytes + 16 <= (int64_t)K * (int)sizeof(T)) {
+        __align__(16) uint32_t w[kBytes / 4 + 4];
+        const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row) + at);
+#pragma unroll
+        for (int i = 0; i < kBytes / 16 + 1; ++i) reinterpret_cast<uint4*>(w)[i] = p[i];
+        shift_down<kBytes / 4>(w, off);
+        const T* x = reinterpret_cast<const T*>(w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_float(x[i]);
     } else {
-        constexpr int N = VEC * (int)sizeof(T) / 16;
-        uint4 raw[N];
-        T* e = reinterpret_cast<T*>(raw);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) e[i] = from_float<T>(v[i]);
+        for (int i = 0; i < 8; ++i) v[i] = e + i >= 0 && e + i < K ? to_float(row[e + i]) : 0.f;
+    }
+}
+template <class T>
+__device__ __forceinline__ void store_any(T* row, int e, int K, const float* v) {
+    const bool whole = e >= 0 && e + 8 <= K;
+    __align__(16) T x[8];
 #pragma unroll
-        for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(p)[i] = raw[i];
+    for (int i = 0; i < 8; ++i) x[i] = from_float<T>(v[i]);
+    if (whole && (reinterpret_cast<uintptr_t>(row + e) & 15u) == 0) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            reinterpret_cast<uint4*>(row + e)[i] = reinterpret_cast<const uint4*>(x)[i];
+    } else if (whole && (reinterpret_cast<uintptr_t>(row + e) & 3u) == 0) {
+#pragma unroll
+        for (int i = 0; i < 2 * (int)sizeof(T); ++i)
+            reinterpret_cast<uint32_t*>(row + e)[i] = reinterpret_cast<const uint32_t*>(x)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e + i >= 0 && e + i < K) row[e + i] = x[i];
     }
 }
 
@@ -71,20 +141,57 @@ __device__ __forceinline__ void store(T* p, const float* v) {
 __device__ __forceinline__ uint32_t code_bits(float v, float inv) {
     return __float_as_uint(__fmaf_rn(v, inv, 12582912.f));
 }
-template <int VEC>
-__device__ __forceinline__ void store_codes(int8_t* p, const float* v, float inv, bool finite) {
-    if constexpr (VEC == 1) {
-        *p = finite ? (int8_t)(code_bits(v[0], inv) & 0xFFu) : (int8_t)0;
-    } else {
-        uint32_t w[VEC / 4];
+__device__ __forceinline__ uint2 codes8(const float* v, float inv, bool finite) {
+    uint32_t w[2];
 #pragma unroll
-        for (int i = 0; i < VEC / 4; ++i) {
-            const uint32_t lo = __byte_perm(code_bits(v[4 * i], inv), code_bits(v[4 * i + 1], inv), 0x0040);
-            const uint32_t hi = __byte_perm(code_bits(v[4 * i + 2], inv), code_bits(v[4 * i + 3], inv), 0x0040);
-            w[i] = finite ? __byte_perm(lo, hi, 0x5410) : 0u;
-        }
-        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __byte_perm(code_bits(v[4 * i], inv), code_bits(v[4 * i + 1], inv), 0x0040);
+        const uint32_t hi = __byte_perm(code_bits(v[4 * i + 2], inv), code_bits(v[4 * i + 3], inv), 0x0040);
+        w[i] = finite ? __byte_perm(lo, hi, 0x5410) : 0u;
     }
+    return make_uint2(w[0], w[1]);
+}
+// The codes of elements [e, e + 8) of a row of K, by a whole warp whose lanes
+// hold consecutive groups: where the row of codes lies off the groups' 8-byte
+// boundaries, each lane stores the aligned word made of its last codes and the
+// next lane's first ones; the ends go byte by byte.
+__device__ __forceinline__ void store_codes_any(int8_t* row, int e, int K, uint2 c) {
+    const int off = (int)(reinterpret_cast<uintptr_t>(row + e) & 7u);  // the same in a warp
+    const bool whole = e >= 0 && e + 8 <= K;
+    int lo = 0, hi = 8;  // codes left for single stores
+    if (off == 0) {
+        if (whole) {
+            *reinterpret_cast<uint2*>(row + e) = c;
+            return;
+        }
+    } else {
+        const int lane = threadIdx.x & 31;
+        const uint32_t next = __shfl_down_sync(0xffffffffu, (int)whole, 1);
+        const uint32_t prev = __shfl_up_sync(0xffffffffu, (int)whole, 1);
+        const uint32_t nx = __shfl_down_sync(0xffffffffu, c.x, 1), ny = __shfl_down_sync(0xffffffffu, c.y, 1);
+        const bool with_next = whole && lane < 31 && next, with_prev = whole && lane > 0 && prev;
+        if (with_next) {
+            // bytes 8 - off .. 8 of mine, then the next lane's
+            const int skip = 8 - off;
+            uint32_t w[4] = {c.x, c.y, nx, ny};
+            if (skip & 4) {
+                w[0] = w[1];
+                w[1] = w[2];
+                w[2] = w[3];
+            }
+            if (skip & 3) {
+                w[0] = __funnelshift_r(w[0], w[1], 8 * (skip & 3));
+                w[1] = __funnelshift_r(w[1], w[2], 8 * (skip & 3));
+            }
+            *reinterpret_cast<uint2*>(row + e + skip) = make_uint2(w[0], w[1]);
+            hi = skip;
+        }
+        if (with_prev) lo = 8 - off;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i >= lo && i < hi && e + i >= 0 && e + i < K)
+            row[e + i] = (int8_t)((i < 4 ? c.x >> (8 * i) : c.y >> (8 * (i - 4))) & 0xFFu);
 }
 
 // g / (1 + e^-g) * u, with the exponential of a number below zero so that
@@ -94,128 +201,263 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return g * __fdividef(g < 0.f ? t : 1.f, 1.f + t) * u;
 }
 
-// One item of a row: VEC values of y (of h * gamma for the norms), the sum of
-// squares of h, and the sum h itself written where the mode has a residual.
-template <class T, int MODE, int VEC>
-__device__ __forceinline__ void item(const RowArgs& a, int64_t row, int e, float* v, float& ss, bool again) {
-    const T* x = static_cast<const T*>(a.x) + row * a.ldx + e;
-    if (MODE == kRowNormResidual) {
-        T* ro = static_cast<T*>(a.ro) + row * a.ldo + e;
-        if (again) {
-            load<T, VEC>(ro, v);
-        } else {
-            float r[VEC];
-            load<T, VEC>(x, v);
-            load<T, VEC>(static_cast<const T*>(a.r) + row * a.ldr + e, r);
+__host__ __device__ constexpr bool two_inputs(int mode) { return mode == kRowNormResidual || mode == kRowSiluMul; }
+__host__ __device__ constexpr bool is_norm(int mode) { return mode == kRowNorm || mode == kRowNormResidual; }
+
+// From the inputs x and r of a group: v = y (h * gamma for the norms) in x's
+// place, the sum of squares of h, and h in r's place where there is a residual.
+template <class T, int MODE>
+__device__ __forceinline__ void combine(float* x, float* r, const float* gamma, float& ss) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = to_float(from_float<T>(v[i] + r[i]));
-            store<T, VEC>(ro, v);
-        }
-    } else {
-        load<T, VEC>(x, v);
-    }
-    if (MODE == kRowSiluMul) {
-        float u[VEC];
-        load<T, VEC>(static_cast<const T*>(a.r) + row * a.ldr + e, u);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = silu_mul(v[i], u[i]);
-    }
-    if (MODE == kRowNorm || MODE == kRowNormResidual) {
-        float g[VEC];
-        load<T, VEC>(static_cast<const T*>(a.gamma) + e, g);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            ss = __fmaf_rn(v[i], v[i], ss);
-            v[i] *= g[i];
+    for (int i = 0; i < 8; ++i) {
+        if (MODE == kRowNormResidual) x[i] = r[i] = to_float(from_float<T>(x[i] + r[i]));
+        if (MODE == kRowSiluMul) x[i] = silu_mul(x[i], r[i]);
+        if (is_norm(MODE)) {
+            ss = __fmaf_rn(x[i], x[i], ss);
+            x[i] *= gamma[i];
         }
     }
 }
 
-// blockDim.x threads per row (a warp, then blockDim.y rows per block; or the
-// whole block), ITEMS vectors of VEC elements each, held in registers;
-// ITEMS = 0: rows of any length, read a second time for the codes.
-template <class T, int MODE, int VEC, int ITEMS>
-__global__ void __launch_bounds__(1024) rows_kernel(const RowArgs a) {
-    __shared__ uint32_t s_max[32];
-    __shared__ float s_sum[32];
-    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (row >= a.M) return;  // whole warps: rows of a block's y share no barrier
-    const int n = blockDim.x;
-    float v[ITEMS > 0 ? ITEMS : 1][VEC];
-    float ss = 0.f;
-    uint32_t top = 0;  // largest |y| as bits: ordered like the values, NaN above infinity
-    auto look = [&](const float* y) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-    };
-    if constexpr (ITEMS > 0) {
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const int e = (i * n + (int)threadIdx.x) * VEC;
-            if (e < a.K) item<T, MODE, VEC>(a, row, e, v[i], ss, false);
-            else
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) v[i][j] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) look(v[i]);
-    } else {
-        for (int64_t e = (int64_t)threadIdx.x * VEC; e < a.K; e += (int64_t)n * VEC) {
-            item<T, MODE, VEC>(a, row, (int)e, v[0], ss, false);
-            look(v[0]);
-        }
-    }
+struct RowScale {
+    float pre, inv;  // codes round(v * pre * inv)
+    bool finite;
+};
+// Reduces the row's maximum and sum over the blockDim.x threads that hold it,
+// and writes its scale. s: 64 words, another set for the row after this one.
+template <int MODE>
+__device__ __forceinline__ RowScale row_scale(const RowArgs& a, int64_t row, uint32_t top, float ss, uint32_t* s) {
     top = __reduce_max_sync(0xffffffffu, top);
-    if (MODE == kRowNorm || MODE == kRowNormResidual) {
+    if (is_norm(MODE)) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     }
-    if (n > 32) {  // the block's warps in one row (blockDim.y == 1)
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = n >> 5;
+    if (blockDim.x > 32) {  // (then blockDim.y is 1)
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
         if (lane == 0) {
-            s_max[warp] = top;
-            s_sum[warp] = ss;
+            s[warp] = top;
+            s[32 + warp] = __float_as_uint(ss);
         }
         __syncthreads();
-        top = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[lane] : 0u);
-        if (MODE == kRowNorm || MODE == kRowNormResidual) {
-            ss = lane < warps ? s_sum[lane] : 0.f;
+        top = __reduce_max_sync(0xffffffffu, lane < warps ? s[lane] : 0u);
+        if (is_norm(MODE)) {
+            ss = lane < warps ? __uint_as_float(s[32 + lane]) : 0.f;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         }
     }
-    bool finite = top < 0x7F800000u;
-    float most = __uint_as_float(top), r = 1.f;
-    if (MODE == kRowNorm || MODE == kRowNormResidual) {
-        finite = finite && ss < INFINITY;
-        r = rsqrtf(ss / (float)a.K + a.eps);
-        most *= r;
-        finite = finite && most < INFINITY;
-    }
-    const float scale = fmaxf(most / 127.f, kMinScale);
-    const float inv = 1.f / scale;  // at most 2^126
-    auto norm = [&](float* y) {
-        if (MODE == kRowNorm || MODE == kRowNormResidual) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) y[j] *= r;
+    // The norm is common to a row's values and its scale: codes come from v and
+    // max|v| alone, so they do not depend on the order of the sum of squares
+    // (unless the scale is at its least).
+    RowScale x;
+    x.finite = top < 0x7F800000u;
+    const float most = __uint_as_float(top);
+    float step = most / 127.f, scale = step;
+    x.pre = 1.f;
+    if (is_norm(MODE)) {
+        const float r = rsqrtf(ss / (float)a.K + a.eps);
+        scale = most * r / 127.f;
+        x.finite = x.finite && ss < INFINITY && scale < INFINITY;
+        if (step < kMinScale || scale < kMinScale) {
+            x.pre = r;
+            step = fmaxf(scale, kMinScale);
         }
+    }
+    scale = fmaxf(scale, kMinScale);
+    x.inv = 1.f / fmaxf(step, kMinScale);  // at most 2^126
+    if (threadIdx.x == 0) a.scale[row] = x.finite ? scale : __uint_as_float(0x7FC00000u);
+    return x;
+}
+template <int MODE>
+__device__ __forceinline__ void look(float* v, uint32_t& top) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);  // NaN above infinity
+}
+template <int MODE>
+__device__ __forceinline__ uint2 codes_of(float* v, const RowScale& s) {
+    if (is_norm(MODE)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= s.pre;
+    }
+    return codes8(v, s.inv, s.finite);
+}
+
+__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// All but the latest `left` (at most 3) groups of this thread's copies have landed.
+__device__ __forceinline__ void wait_copies(int left) {
+    if (left >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+constexpr int kMaxStages = 4;
+
+// blockDim.x threads per row (one warp, then blockDim.y rows at a time; or the
+// whole block), ITEMS groups each, `stages` rows ahead. EDGE: rows do not all
+// start on a 16-byte boundary (or end a whole group); x, r and ro lie at the same
+// offset from one. Otherwise they do, K % 8 == 0 and the codes' rows lie on 8-byte
+// boundaries.
+template <class T, int MODE, int ITEMS, bool EDGE>
+__global__ void __launch_bounds__(ITEMS == 1 || (ITEMS == 2 && sizeof(T) == 2) ? 1024 : 512)
+    rows_kernel(const RowArgs a, const int stages) {
+    extern __shared__ uint4 slots[];  // [stage][input][item][16 bytes of a group][thread]
+    __shared__ uint32_t s[2][64];
+    constexpr int kIn = two_inputs(MODE) ? 2 : 1, kW = (int)sizeof(T) / 2;
+    const int n = blockDim.x, all = n * blockDim.y;
+    uint4* mine = slots + threadIdx.y * n + threadIdx.x;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // first element of this thread's group i of a row
+    auto lead = [&](int64_t m) {
+        return EDGE ? (int)(reinterpret_cast<uintptr_t>(static_cast<const T*>(a.x) + m * a.ldx) & 15u) / (int)sizeof(T) : 0;
     };
-    if (threadIdx.x == 0) a.scale[row] = finite ? scale : __uint_as_float(0x7FC00000u);
-    int8_t* q = a.q + row * a.ldq;
-    if constexpr (ITEMS > 0) {
+    auto group = [&](int i, int off) { return (i * n + (int)threadIdx.x) * 8 - off; };
+    auto whole = [&](int e) { return EDGE ? e >= 0 && e + 8 <= a.K : e < a.K; };
+    auto fetch = [&](int64_t m, int st) {
+        if (m < a.M) {
+            const int off = lead(m);
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) {
+                const int e = group(i, off);
+                if (!whole(e)) continue;
+#pragma unroll
+                for (int w = 0; w < kW; ++w) {
+                    copy16(mine + (((st * kIn + 0) * ITEMS + i) * kW + w) * all,
+                           reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + m * a.ldx + e) + w);
+                    if (kIn == 2)
+                        copy16(mine + (((st * kIn + 1) * ITEMS + i) * kW + w) * all,
+                               reinterpret_cast<const uint4*>(static_cast<const T*>(a.r) + m * a.ldr + e) + w);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto slot = [&](int st, int in, int i) {
+        Raw<T> r;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) r.w[w] = mine[(((st * kIn + in) * ITEMS + i) * kW + w) * all];
+        return r;
+    };
+    for (int st = 0; st < stages; ++st) fetch(row + st * step, st);
+    Raw<T> gamma[ITEMS];
+    if (is_norm(MODE) && !EDGE) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            if (group(i, 0) < a.K) gamma[i] = load_raw(static_cast<const T*>(a.gamma) + group(i, 0));
+    }
+    int st = 0;
+    for (int turn = 0; row < a.M; row += step, turn ^= 1) {
+        const int off = lead(row);
+        float v[ITEMS][8], ss = 0.f;
+        uint32_t top = 0;
+        wait_copies(stages - 1);
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const int e = (i * n + (int)threadIdx.x) * VEC;
-            norm(v[i]);
-            if (e < a.K) store_codes<VEC>(q + e, v[i], inv, finite);
+            const int e = group(i, off);
+            float o[8], g[8];
+            if (whole(e)) {
+                unpack(slot(st, 0, i), v[i]);
+                if (kIn == 2) unpack(slot(st, 1, i), o);
+                if (is_norm(MODE)) {
+                    if (EDGE) load_any(static_cast<const T*>(a.gamma), e, a.K, g);
+                    else unpack(gamma[i], g);
+                }
+            } else if constexpr (!EDGE) {
+                continue;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const bool in = e + k >= 0 && e + k < a.K;
+                    v[i][k] = in ? to_float(static_cast<const T*>(a.x)[row * a.ldx + e + k]) : 0.f;
+                    if (kIn == 2) o[k] = in ? to_float(static_cast<const T*>(a.r)[row * a.ldr + e + k]) : 0.f;
+                    if (is_norm(MODE)) g[k] = in ? to_float(static_cast<const T*>(a.gamma)[e + k]) : 0.f;
+                }
+            }
+            combine<T, MODE>(v[i], o, g, ss);
+            if (MODE == kRowNormResidual) {
+                T* ro = static_cast<T*>(a.ro) + row * a.ldo + e;
+                if (whole(e)) {
+                    store_raw(ro, o);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (e + k >= 0 && e + k < a.K) ro[k] = from_float<T>(o[k]);
+                }
+            }
+            look<MODE>(v[i], top);
         }
-    } else {
-        for (int64_t e = (int64_t)threadIdx.x * VEC; e < a.K; e += (int64_t)n * VEC) {
-            item<T, MODE, VEC>(a, row, (int)e, v[0], ss, true);
-            norm(v[0]);
-            store_codes<VEC>(q + e, v[0], inv, finite);
+        const RowScale sc = row_scale<MODE>(a, row, top, ss, s[turn]);
+        // (every lane's reads of the slots are behind it: their values went into the reduction)
+        fetch(row + stages * step, st);
+        st = st + 1 == stages ? 0 : st + 1;
+        int8_t* q = a.q + row * a.ldq;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int e = group(i, off);
+            if (EDGE) store_codes_any(q, e, a.K, codes_of<MODE>(v[i], sc));
+            else if (e < a.K) *reinterpret_cast<uint2*>(q + e) = codes_of<MODE>(v[i], sc);
+        }
+    }
+    wait_copies(0);
+}
+
+// Inputs at any alignment, in groups that lie on x's 16-byte boundaries.
+// ITEMS = 0: rows of any length, read a second time for the codes.
+template <class T, int MODE, int ITEMS>
+__global__ void __launch_bounds__(512) rows_any_kernel(const RowArgs a) {
+    __shared__ uint32_t s[2][64];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    const int n = blockDim.x;
+    int turn = 0;
+    for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < a.M; row += step, turn ^= 1) {
+        const T* xr = static_cast<const T*>(a.x) + row * a.ldx;
+        const int off = (int)(reinterpret_cast<uintptr_t>(xr) & 15u) / (int)sizeof(T);
+        auto group = [&](int e, float* v, float& ss, bool again) {
+            float o[8], g[8];
+            if (MODE == kRowNormResidual && again) {
+                load_any(static_cast<const T*>(a.ro) + row * a.ldo, e, a.K, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = 0.f;
+            } else {
+                load_any(xr, e, a.K, v);
+                if (two_inputs(MODE)) load_any(static_cast<const T*>(a.r) + row * a.ldr, e, a.K, o);
+            }
+            if (is_norm(MODE)) load_any(static_cast<const T*>(a.gamma), e, a.K, g);
+            combine<T, MODE>(v, o, g, ss);
+            if (MODE == kRowNormResidual && !again) store_any(static_cast<T*>(a.ro) + row * a.ldo, e, a.K, o);
+        };
+        float ss = 0.f;
+        uint32_t top = 0;
+        if constexpr (ITEMS > 0) {
+            float v[ITEMS][8];
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) {
+                group((i * n + (int)threadIdx.x) * 8 - off, v[i], ss, false);
+                look<MODE>(v[i], top);
+            }
+            const RowScale sc = row_scale<MODE>(a, row, top, ss, s[turn]);
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i)
+                store_codes_any(a.q + row * a.ldq, (i * n + (int)threadIdx.x) * 8 - off, a.K, codes_of<MODE>(v[i], sc));
+        } else {
+            // whole warps take part to the end, for the exchange between lanes
+            const int64_t end = ((int64_t)a.K + off + 8 * n - 1) / (8 * n) * (8 * n);
+            float v[8], unused = 0.f;
+            for (int64_t e = (int64_t)threadIdx.x * 8; e < end; e += 8 * n) {
+                group((int)e - off, v, ss, false);
+                look<MODE>(v, top);
+            }
+            const RowScale sc = row_scale<MODE>(a, row, top, ss, s[turn]);
+            for (int64_t e = (int64_t)threadIdx.x * 8; e < end; e += 8 * n) {
+                group((int)e - off, v, unused, true);
+                store_codes_any(a.q + row * a.ldq, (int)e - off, a.K, codes_of<MODE>(v, sc));
+            }
         }
     }
 }
@@ -223,10 +465,11 @@ __global__ void __launch_bounds__(1024) rows_kernel(const RowArgs a) {
 // A launch whose set-up may overlap the stream's previous kernel (the kernels
 // wait for it before they touch memory).
 template <class... Params, class... Args>
-cudaError_t go(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t st, Args... args) {
+cudaError_t go(void (*kernel)(Params...), dim3 grid, dim3 block, int smem, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -236,52 +479,105 @@ cudaError_t go(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t st
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Persistent blocks: as many as are resident without dynamic shared memory,
+// found once per kernel and block size (by warps per block).
+template <class... Params>
+cudaError_t resident(void (*kernel)(Params...), int threads, std::atomic<int>* known, int* per_sm) {
+    int n = known[threads / 32].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0);
+        if (e != cudaSuccess) return e;
+        n = n < 1 ? 1 : n;
+        known[threads / 32].store(n, std::memory_order_relaxed);
+    }
+    *per_sm = n;
+    return cudaSuccess;
+}
+
+constexpr int kSlotBytes = 200 * 1024;  // shared memory of an SM's slots
+
+template <class T, int MODE, int ITEMS, bool EDGE>
+cudaError_t launch_slots(const RowArgs& a, dim3 block, int sms, cudaStream_t st) {
+    static std::atomic<int> known[33];
+    static std::atomic<bool> allowed[64];  // by device: more than 48 KB of shared memory
+    auto kernel = rows_kernel<T, MODE, ITEMS, EDGE>;
+    const int threads = (int)(block.x * block.y);
+    int dev = 0, per_sm = 1;
+    cudaError_t e = resident(kernel, threads, known, &per_sm);
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !allowed[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlotBytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) allowed[dev].store(true, std::memory_order_relaxed);
+    }
+    const int bytes = threads * ITEMS * 8 * (int)sizeof(T) * (two_inputs(MODE) ? 2 : 1);  // of one stage
+    while (per_sm > 1 && per_sm * bytes > kSlotBytes) --per_sm;
+    const int64_t rows = (a.M + block.y - 1) / block.y, most = (int64_t)sms * per_sm;
+    const unsigned grid = (unsigned)(rows < most ? rows : most);
+    // rows ahead: what fits, and no more than a block has
+    const int64_t turns = (rows + grid - 1) / grid;
+    int stages = kSlotBytes / (per_sm * bytes);
+    stages = stages < kMaxStages ? stages : kMaxStages;
+    stages = stages < turns ? stages : (int)turns;
+    return go(kernel, dim3(grid), block, stages * bytes, st, a, stages);
+}
+
+template <class T, int MODE, int ITEMS>
+cudaError_t launch_any(const RowArgs& a, dim3 block, int sms, cudaStream_t st) {
+    static std::atomic<int> known[33];
+    auto kernel = rows_any_kernel<T, MODE, ITEMS>;
+    int per_sm = 1;
+    const cudaError_t e = resident(kernel, (int)(block.x * block.y), known, &per_sm);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = (a.M + block.y - 1) / block.y, most = (int64_t)sms * per_sm;
+    return go(kernel, dim3((unsigned)(rows < most ? rows : most)), block, 0, st, a);
+}
+
 template <class T, int MODE>
 cudaError_t launch_rows(const RowArgs& a, int sms, cudaStream_t st) {
-    auto wide = [](const void* p, int64_t ld) {
-        return !p || ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * (int64_t)sizeof(T))) & 15u) == 0;
+    auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+    auto pitch = [](int64_t ld) { return (uintptr_t)(ld * (int64_t)sizeof(T)); };
+    // r and ro at x's offset from a 16-byte boundary in every row
+    auto with_x = [&](const void* p, int64_t ld) {
+        return !p || (((at(p) - at(a.x)) | (pitch(ld) - pitch(a.ldx))) & 15u) == 0;
     };
-    const bool vec = a.K % 8 == 0 && wide(a.x, a.ldx) && wide(a.r, a.ldr) && wide(a.ro, a.ldo) && wide(a.gamma, 0) &&
-                     ((reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)a.ldq) & 7u) == 0;
-    const int64_t items = vec ? a.K / 8 : a.K;  // vectors in a row
-    dim3 block(32, 1), grid((unsigned)a.M);
-    cudaError_t e = cudaSuccess;
-    auto per_row = [&](int each) { return (int)((items + each - 1) / each + 31) / 32 * 32; };
-    if (vec) {
-        if (items <= 128) {
-            block.y = (unsigned)(a.M < 8 ? a.M : 8);
-            grid.x = (unsigned)((a.M + block.y - 1) / block.y);
-            if (items <= 32) e = go(rows_kernel<T, MODE, 8, 1>, grid, block, st, a);
-            else if (items <= 64) e = go(rows_kernel<T, MODE, 8, 2>, grid, block, st, a);
-            else e = go(rows_kernel<T, MODE, 8, 4>, grid, block, st, a);
-            return e;
-        }
-        const int most = a.M <= sms ? 1024 : 512;
-        if (per_row(1) <= most) {
-            block.x = per_row(1);
-            e = go(rows_kernel<T, MODE, 8, 1>, grid, block, st, a);
-        } else if (per_row(2) <= most) {
-            block.x = per_row(2);
-            e = go(rows_kernel<T, MODE, 8, 2>, grid, block, st, a);
-        } else if (per_row(4) <= 1024) {
-            block.x = per_row(4);
-            e = go(rows_kernel<T, MODE, 8, 4>, grid, block, st, a);
-        } else {
-            block.x = 1024;
-            e = go(rows_kernel<T, MODE, 8, 0>, grid, block, st, a);
-        }
-    } else if (items <= 32 * 16) {
+    const bool same = with_x(a.r, a.ldr) && with_x(a.ro, a.ldo);
+    const bool aligned = same && a.K % 8 == 0 && ((at(a.x) | pitch(a.ldx) | at(a.gamma)) & 15u) == 0 &&
+                         ((at(a.q) | (uintptr_t)a.ldq) & 7u) == 0;
+    // groups of eight in a row, one more where the first may be partial
+    const int64_t groups = aligned ? a.K / 8 : ((int64_t)a.K + 7) / 8 + 1;
+    auto threads = [&](int items) { return (groups + items - 1) / items + 31 & ~(int64_t)31; };
+    dim3 block(32, 1);
+    int items = 0;
+    const int most2 = sizeof(T) == 2 ? 1024 : 512;
+    if (groups <= 64) {
+        // a warp per row, eight rows per block
+        items = groups <= 32 ? 1 : 2;
         block.y = (unsigned)(a.M < 8 ? a.M : 8);
-        grid.x = (unsigned)((a.M + block.y - 1) / block.y);
-        e = go(rows_kernel<T, MODE, 1, 16>, grid, block, st, a);
-    } else if (items <= 1024 * 16) {
-        block.x = per_row(16);
-        e = go(rows_kernel<T, MODE, 1, 16>, grid, block, st, a);
-    } else {
-        block.x = 1024;
-        e = go(rows_kernel<T, MODE, 1, 0>, grid, block, st, a);
+    } else if (threads(1) <= 1024 && a.M <= sms) {
+        items = 1;  // few rows: the shortest way through one
+    } else if (threads(2) <= most2) {
+        items = 2;
+    } else if (threads(4) <= 512) {
+        items = 4;
     }
-    return e;
+    if (items > 0 && block.y == 1) block.x = groups <= 64 ? 32 : (unsigned)threads(items);
+    if (items == 0 || !same) {
+        if (items == 0 || items == 4 || threads(2) > 512) {
+            block = dim3(512, 1);
+            return launch_any<T, MODE, 0>(a, block, sms, st);
+        }
+        if (block.x > 32) block.x = (unsigned)threads(2);
+        return launch_any<T, MODE, 2>(a, block, sms, st);
+    }
+    if (aligned)
+        return items == 1   ? launch_slots<T, MODE, 1, false>(a, block, sms, st)
+               : items == 2 ? launch_slots<T, MODE, 2, false>(a, block, sms, st)
+                            : launch_slots<T, MODE, 4, false>(a, block, sms, st);
+    return items == 1   ? launch_slots<T, MODE, 1, true>(a, block, sms, st)
+           : items == 2 ? launch_slots<T, MODE, 2, true>(a, block, sms, st)
+                        : launch_slots<T, MODE, 4, true>(a, block, sms, st);
 }
 
 template <class T>
@@ -292,42 +588,75 @@ cudaError_t launch_rows_type(const RowArgs& a, int mode, int sms, cudaStream_t s
                                       : launch_rows<T, kRowSiluMul>(a, sms, st);
 }
 
-// values = code * scale, one product and one rounding per element.
-template <class T, int VEC>
-__global__ void __launch_bounds__(256) dequantize_kernel(const int8_t* q, int64_t ldq, const float* scale, int K,
-                                                         int chunks, T* out, int64_t ldo) {
+// values = code * scale, one product and one rounding per element, in groups
+// on the output's 16-byte boundaries. A thread takes kDeq groups, a block's row
+// apart: their loads are in flight together.
+constexpr int kDeq = 4;
+template <class T>
+__global__ void __launch_bounds__(256) dequantize_kernel(const int8_t* q, int64_t ldq, const float* scale, int64_t M,
+                                                         int K, int chunks, T* out, int64_t ldo) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t row = blockIdx.x / chunks;
-    const int e = ((int)(blockIdx.x % chunks) * 256 + (int)threadIdx.x) * VEC;
-    if (e >= K) return;
+    const int64_t row = (int64_t)(blockIdx.x / chunks) * blockDim.y + threadIdx.y;
+    if (row >= M) return;
     const float s = scale[row];
-    float v[VEC];
-    if constexpr (VEC == 1) {
-        v[0] = (float)q[row * ldq + e] * s;
-    } else {
-        const uint2 raw = *reinterpret_cast<const uint2*>(q + row * ldq + e);
+    const int8_t* qr = q + row * ldq;
+    T* orow = out + row * ldo;
+    const int first = (int)(blockIdx.x % chunks) * (int)blockDim.x * kDeq + (int)threadIdx.x;
+    const int lead = (int)(reinterpret_cast<uintptr_t>(orow) & 15u) / (int)sizeof(T);
+    uint32_t w[kDeq][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = (float)(int8_t)(raw.x >> (8 * i)) * s;
-            v[4 + i] = (float)(int8_t)(raw.y >> (8 * i)) * s;
+    for (int i = 0; i < kDeq; ++i) {
+        const int e = (first + i * (int)blockDim.x) * 8 - lead;
+        const int off = (int)(reinterpret_cast<uintptr_t>(qr + e) & 7u);
+        if (e >= K) continue;
+        if (off == 0 && e >= 0 && e + 8 <= K) {
+            *reinterpret_cast<uint2*>(w[i]) = *reinterpret_cast<const uint2*>(qr + e);
+        } else if (e - off >= 0 && e - off + 16 <= K) {
+            *reinterpret_cast<uint2*>(w[i]) = *reinterpret_cast<const uint2*>(qr + e - off);
+            *reinterpret_cast<uint2*>(w[i] + 2) = *reinterpret_cast<const uint2*>(qr + e - off + 8);
+            if (off & 4) {
+                w[i][0] = w[i][1];
+                w[i][1] = w[i][2];
+                w[i][2] = w[i][3];
+            }
+            if (off & 3) {
+                w[i][0] = __funnelshift_r(w[i][0], w[i][1], 8 * (off & 3));
+                w[i][1] = __funnelshift_r(w[i][1], w[i][2], 8 * (off & 3));
+            }
+        } else {
+            w[i][0] = w[i][1] = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (e + k >= 0 && e + k < K) w[i][k >> 2] |= (uint32_t)(uint8_t)qr[e + k] << (8 * (k & 3));
         }
     }
-    store<T, VEC>(out + row * ldo + e, v);
+#pragma unroll
+    for (int i = 0; i < kDeq; ++i) {
+        const int e = (first + i * (int)blockDim.x) * 8 - lead;
+        if (e >= K) continue;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = (float)(int8_t)(w[i][k >> 2] >> (8 * (k & 3))) * s;
+        store_any(orow, e, K, v);
+    }
 }
 
 template <class T>
 cudaError_t launch_deq(const int8_t* q, int64_t ldq, const float* scale, int64_t M, int K, T* out, int64_t ldo,
                        cudaStream_t st) {
-    const bool vec = K % 8 == 0 && ((reinterpret_cast<uintptr_t>(q) | (uintptr_t)ldq) & 7u) == 0 &&
-                     ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(ldo * (int64_t)sizeof(T))) & 15u) == 0;
-    const int chunks = (int)(((int64_t)K + (vec ? 2047 : 255)) / (vec ? 2048 : 256));
+    // a block is 256 threads: as many to a row as give each kDeq groups, at least a warp
+    const int64_t groups = ((int64_t)K + 7) / 8 + 1;
+    unsigned x = 32;
+    while (x < 256 && x * kDeq < groups) x *= 2;
+    const dim3 block(x, M < 256 / x ? (unsigned)M : 256 / x);
+    const int chunks = (int)((groups + x * kDeq - 1) / (x * kDeq));
     // whole rows per launch, within the grid's limit of 2^31 - 1 blocks
-    const int64_t most = 2147483647ll / chunks;
+    const int64_t most = 2147483647ll / chunks * block.y;
     for (int64_t m0 = 0; m0 < M; m0 += most) {
-        const unsigned grid = (unsigned)((M - m0 < most ? M - m0 : most) * chunks);
-        const cudaError_t e = go(vec ? dequantize_kernel<T, 8> : dequantize_kernel<T, 1>, dim3(grid), dim3(256), st,
-                                 q + m0 * ldq, ldq, scale + m0, K, chunks, out + m0 * ldo, ldo);
+        const int64_t rows = M - m0 < most ? M - m0 : most;
+        const cudaError_t e = go(dequantize_kernel<T>, dim3((unsigned)((rows + block.y - 1) / block.y * chunks)), block, 0, st,
+                                 q + m0 * ldq, ldq, scale + m0, rows, K, chunks, out + m0 * ldo, ldo);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
