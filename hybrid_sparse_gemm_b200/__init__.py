@@ -103,6 +103,18 @@ for _n in ["patch_pack", "patch_linear", "patch_linear_path", "patch_linear_host
     getattr(_lib, _n).restype = ctypes.c_int
 
 
+try:
+    from . import _binding
+except ImportError as e:
+    raise ImportError(f"{os.path.join(_HERE, '_binding.so')} is missing or does not load: build it with "
+                      "`python -m hybrid_sparse_gemm_b200.build`") from e
+_binding.init((torch.bfloat16, torch.float16, torch.float32, torch.int8), torch.cuda.current_device,
+              getattr(torch._C, "_cuda_getCurrentRawStream", None),
+              tuple(ctypes.cast(getattr(_lib, n), _P).value for n in
+                    ("patch_linear_q8", "patch_quantize_q8", "patch_rmsnorm_q8", "patch_silu_mul_q8",
+                     "patch_dequantize_q8")))
+
+
 class PatchError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {msg}")
@@ -283,12 +295,6 @@ def _scales(name: str, t: torch.Tensor, n: int):
         raise ValueError(f"{name} must be {n} contiguous scales")
 
 
-def _row_type(x: torch.Tensor) -> int:
-    if x.dim() != 2 or x.dtype not in _TYPES:
-        raise TypeError(f"need a 2-D bf16, fp16 or fp32 tensor, not {x.dim()}-D {x.dtype}")
-    return _TYPES[x.dtype]
-
-
 def patch_pack_q8(W: torch.Tensor, mask_bits: torch.Tensor, tile_flags, tile_rows: int = 128, tile_cols: int = 128,
                   bitorder: int = 0, w_scale: torch.Tensor | None = None, stream=None) -> int:
     """Returns an opaque handle (int). W [N,K] on the device: bf16, quantised per
@@ -317,8 +323,7 @@ def patch_pack_q8(W: torch.Tensor, mask_bits: torch.Tensor, tile_flags, tile_row
 
 def patch_linear_q8(h: int, X: torch.Tensor, x_scale: torch.Tensor, Y: torch.Tensor, path: int = PATH_AUTO, stream=None):
     """Y [M,N] (bf16, fp16 or fp32) from the codes X [M,K] and their scales [M]."""
-    _check(_lib.patch_linear_q8(h, X.data_ptr(), X.stride(0), x_scale.data_ptr(), X.shape[0], Y.data_ptr(),
-                                Y.stride(0), _TYPES[Y.dtype], path, _stream(stream)))
+    _check(_binding.linear_q8(h, Y.shape[1], X.shape[1], X, x_scale, Y, path, stream))
 
 
 def patch_unpack_q8(h: int, W: torch.Tensor, w_scale: torch.Tensor, stream=None):
@@ -327,53 +332,24 @@ def patch_unpack_q8(h: int, W: torch.Tensor, w_scale: torch.Tensor, stream=None)
 
 def patch_quantize_q8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None):
     """Codes q [M,K] (int8) and scales [M] (fp32) of the rows of x."""
-    t = _row_type(x)
-    _on_device(x, q, scale)
-    _scales("scale", scale, x.shape[0])
-    _check(_lib.patch_quantize_q8(x.data_ptr(), _rows("x", x, x.shape, x.dtype), t, x.shape[0], x.shape[1],
-                                  q.data_ptr(), _rows("q", q, x.shape, torch.int8), scale.data_ptr(), _stream(stream)))
+    _check(_binding.quantize_q8(x, q, scale, stream))
 
 
 def patch_rmsnorm_q8(x: torch.Tensor, gamma: torch.Tensor, eps: float, q: torch.Tensor, scale: torch.Tensor,
                      residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None, stream=None):
     """Codes and scales of the RMS norm of x, or of x + residual, which is then
     written to residual_out (which may be x or residual itself)."""
-    t = _row_type(x)
-    _on_device(x, gamma, q, scale, residual, residual_out)
-    M, K = x.shape
-    _scales("scale", scale, M)
-    if gamma.dtype is not x.dtype or gamma.shape != (K,) or (K > 1 and gamma.stride(0) != 1):
-        raise ValueError(f"gamma must be {K} contiguous elements of {x.dtype}")
-    if (residual is None) != (residual_out is None):
-        raise ValueError("residual and residual_out go together")
-    r, ldr, ro, ldo = None, 0, None, 0
-    if residual is not None:
-        r, ldr = residual.data_ptr(), _rows("residual", residual, x.shape, x.dtype)
-        ro, ldo = residual_out.data_ptr(), _rows("residual_out", residual_out, x.shape, x.dtype)
-    _check(_lib.patch_rmsnorm_q8(x.data_ptr(), _rows("x", x, x.shape, x.dtype), r, ldr, ro, ldo, gamma.data_ptr(), t,
-                                 eps, M, K, q.data_ptr(), _rows("q", q, x.shape, torch.int8), scale.data_ptr(),
-                                 _stream(stream)))
+    _check(_binding.rmsnorm_q8(x, gamma, eps, q, scale, residual, residual_out, stream))
 
 
 def patch_silu_mul_q8(gate: torch.Tensor, up: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None):
     """Codes and scales of silu(gate) * up."""
-    t = _row_type(gate)
-    _on_device(gate, up, q, scale)
-    _scales("scale", scale, gate.shape[0])
-    _check(_lib.patch_silu_mul_q8(gate.data_ptr(), _rows("gate", gate, gate.shape, gate.dtype), up.data_ptr(),
-                                  _rows("up", up, gate.shape, gate.dtype), t, gate.shape[0], gate.shape[1],
-                                  q.data_ptr(), _rows("q", q, gate.shape, torch.int8), scale.data_ptr(),
-                                  _stream(stream)))
+    _check(_binding.silu_mul_q8(gate, up, q, scale, stream))
 
 
 def patch_dequantize_q8(q: torch.Tensor, scale: torch.Tensor, out: torch.Tensor, stream=None):
     """out = q * scale, row by row (bf16, fp16 or fp32)."""
-    t = _row_type(out)
-    _on_device(q, scale, out)
-    _scales("scale", scale, out.shape[0])
-    _check(_lib.patch_dequantize_q8(q.data_ptr(), _rows("q", q, out.shape, torch.int8), scale.data_ptr(), out.shape[0],
-                                    out.shape[1], out.data_ptr(), _rows("out", out, out.shape, out.dtype), t,
-                                    _stream(stream)))
+    _check(_binding.dequantize_q8(q, scale, out, stream))
 
 
 def _codes_like(x: torch.Tensor):
@@ -519,14 +495,9 @@ class PackedLinearQ8:
             out_dtype = out_dtype or X.dtype
             X, x_scale = _codes_like(x)
             patch_quantize_q8(x, X, x_scale, stream)
-        M = X.shape[0]
         if out is None:
-            out = torch.empty((M, self.N), dtype=out_dtype or torch.bfloat16, device=X.device)
-        _rows("X", X, (M, self.K), torch.int8)
-        _rows("out", out, (M, self.N), out.dtype)
-        _scales("x_scale", x_scale, M)
-        _on_device(X, x_scale, out)
-        patch_linear_q8(self.handle, X, x_scale, out, path, stream)
+            out = torch.empty((X.shape[0], self.N), dtype=out_dtype or torch.bfloat16, device=X.device)
+        _check(_binding.linear_q8(self.handle, self.N, self.K, X, x_scale, out, path, stream))
         return out
 
     def unpack(self, stream=None):

@@ -1,4 +1,5 @@
-"""Build libpatch_hybrid.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build libpatch_hybrid.so (the C-ABI library) in-tree with nvcc for sm_100a,
+and _binding.so (the Python argument marshalling of its 8-bit calls) with gcc.
 
     python -m hybrid_sparse_gemm_b200.build [--force]
 """
@@ -8,11 +9,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libpatch_hybrid.so")
+BINDING = os.path.join(HERE, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+CC = os.environ.get("CC", "gcc")
 
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -32,24 +36,30 @@ def headers():
                   glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 
-def stale() -> bool:
-    if not os.path.exists(LIB):
+def stale(out: str, inputs) -> bool:
+    if not os.path.exists(out):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in sources() + headers() + [__file__])
+    t = os.path.getmtime(out)
+    return any(os.path.getmtime(f) > t for f in [*inputs, __file__])
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not stale():
-        return LIB
-    cmd = [NVCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc"),
-           "-o", LIB + ".tmp", *sources()]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+def _run(cmd, out: str, what: str, verbose: bool):
+    r = subprocess.run([*cmd, "-o", out + ".tmp"], capture_output=True, text=True)
     if verbose or r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
     if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + r.stderr[-6000:])
-    os.replace(LIB + ".tmp", LIB)
+        raise RuntimeError(f"{what} failed:\n" + r.stderr[-6000:])
+    os.replace(out + ".tmp", out)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    include = os.path.join(ROOT, "include")
+    binding = os.path.join(HERE, "csrc", "binding.c")
+    if force or stale(LIB, sources() + headers()):
+        _run([NVCC, *FLAGS, "-I", include, "-I", os.path.join(HERE, "csrc"), *sources()], LIB, "nvcc", verbose)
+    if force or stale(BINDING, [binding] + headers()):
+        _run([CC, "-O2", "-Wall", "-shared", "-fPIC", "-I", include, "-I", sysconfig.get_paths()["include"], binding],
+             BINDING, CC, verbose)
     return LIB
 
 

@@ -369,13 +369,13 @@ def test_row_refusals(hsg):
                 lambda: hsg.patch_quantize_q8(x, q, s[:3]), lambda: hsg.patch_quantize_q8(x, q.cpu(), s),
                 lambda: hsg.patch_quantize_q8(x.expand(4, 64)[:, :1].expand(4, 64), q, s),
                 lambda: hsg.patch_silu_mul_q8(x, x[:3], q, s), lambda: hsg.patch_rmsnorm_q8(x, gamma[:63], EPS, q, s),
-                lambda: hsg.patch_rmsnorm_q8(x, gamma.half(), EPS, q, s),
                 lambda: hsg.patch_rmsnorm_q8(x, gamma, EPS, q, s, residual=x),
                 lambda: hsg.patch_dequantize_q8(q, s[:3], x)):
         with pytest.raises(ValueError):
             bad()
     for bad in (lambda: hsg.patch_quantize_q8(x, q.view(torch.uint8), s), lambda: hsg.patch_quantize_q8(x, q, s.half()),
-                lambda: hsg.patch_silu_mul_q8(x, x.half(), q, s), lambda: hsg.patch_dequantize_q8(q, s, x.double())):
+                lambda: hsg.patch_silu_mul_q8(x, x.half(), q, s),
+                lambda: hsg.patch_rmsnorm_q8(x, gamma.half(), EPS, q, s), lambda: hsg.patch_dequantize_q8(q, s, x.double())):
         with pytest.raises(TypeError):
             bad()
     with pytest.raises(hsg.PatchError):

@@ -82,13 +82,19 @@ def test_no_rows_is_a_no_op(lib, op):
     assert ROWS[op](lib, M=0, x=None, q=None, scale=None) == 0
 
 
-def test_python_types(lib):
+def test_cpu_tensors(lib):
     import torch
     import hybrid_sparse_gemm_b200 as hsg
-    x = torch.zeros(4, 64)
-    with pytest.raises(TypeError):
-        hsg.patch_quantize_q8(x.double(), None, None)
-    with pytest.raises(TypeError):
-        hsg.patch_quantize_q8(x[0], None, None)
+    x, q, s = torch.zeros(4, 64), torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4)
+    for call in (lambda: hsg.patch_quantize_q8(x, q, s), lambda: hsg.patch_silu_mul_q8(x, x, q, s),
+                 lambda: hsg.patch_rmsnorm_q8(x, x[0], 1e-5, q, s), lambda: hsg.patch_dequantize_q8(q, s, x),
+                 lambda: hsg.patch_linear_q8(1, q, s, x)):
+        with pytest.raises(ValueError):
+            call()
     with pytest.raises(TypeError):
         hsg.patch_pack_q8(x, None, None)
+    for bad in (lambda: hsg._binding.quantize_q8(x, q, s), lambda: hsg.patch_rmsnorm_q8(x, x[0], "eps", q, s)):
+        with pytest.raises(TypeError):
+            bad()
+    with pytest.raises(AttributeError):
+        hsg.patch_quantize_q8(3, q, s)
