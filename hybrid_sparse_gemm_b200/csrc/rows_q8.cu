@@ -12,11 +12,13 @@
 //
 // The kernels are bound by HBM for many rows and by latency for few. A row is
 // spread over as many threads as give each one or two groups of eight
-// elements; blocks are persistent, and every thread copies its groups of the
-// next rows into its own slots of shared memory (cp.async, no barrier), so that
-// loads stay in flight across the reductions without holding registers. Rows
-// that do not lie on 16-byte boundaries are taken in groups that do (the first
-// and the last one partial); what lies at another offset is shifted into place.
+// elements (four where the values stay packed); blocks are persistent and read
+// their next row before they reduce the present one, so that loads stay in
+// flight across the barrier. For many rows the instructions count as much as
+// the bytes: about ten an element fill the issue slots that 6.5 TB/s leave.
+// Rows that do not lie on 16-byte boundaries are taken in groups that do (the
+// first and the last one partial); what lies at another offset is shifted into
+// place.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -152,69 +154,123 @@ __device__ __forceinline__ uint2 codes8(const float* v, float inv, bool finite) 
     return make_uint2(w[0], w[1]);
 }
 // The codes of elements [e, e + 8) of a row of K, by a whole warp whose lanes
-// hold consecutive groups: where the row of codes lies off the groups' 8-byte
+// hold consecutive groups. Where the row of codes lies off the groups' 8-byte
 // boundaries, each lane stores the aligned word made of its last codes and the
-// next lane's first ones; the ends go byte by byte.
+// next lane's first ones; a warp's outermost codes go in pieces of 4, 2 and 1,
+// and groups that are not whole byte by byte.
 __device__ __forceinline__ void store_codes_any(int8_t* row, int e, int K, uint2 c) {
-    const int off = (int)(reinterpret_cast<uintptr_t>(row + e) & 7u);  // the same in a warp
+    int8_t* p = row + e;
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 7u);  // the same in a warp
     const bool whole = e >= 0 && e + 8 <= K;
-    int lo = 0, hi = 8;  // codes left for single stores
     if (off == 0) {
-        if (whole) {
-            *reinterpret_cast<uint2*>(row + e) = c;
-            return;
-        }
+        if (whole) *reinterpret_cast<uint2*>(p) = c;
     } else {
-        const int lane = threadIdx.x & 31;
-        const uint32_t next = __shfl_down_sync(0xffffffffu, (int)whole, 1);
-        const uint32_t prev = __shfl_up_sync(0xffffffffu, (int)whole, 1);
-        const uint32_t nx = __shfl_down_sync(0xffffffffu, c.x, 1), ny = __shfl_down_sync(0xffffffffu, c.y, 1);
-        const bool with_next = whole && lane < 31 && next, with_prev = whole && lane > 0 && prev;
-        if (with_next) {
-            // bytes 8 - off .. 8 of mine, then the next lane's
-            const int skip = 8 - off;
-            uint32_t w[4] = {c.x, c.y, nx, ny};
-            if (skip & 4) {
-                w[0] = w[1];
-                w[1] = w[2];
-                w[2] = w[3];
-            }
-            if (skip & 3) {
-                w[0] = __funnelshift_r(w[0], w[1], 8 * (skip & 3));
-                w[1] = __funnelshift_r(w[1], w[2], 8 * (skip & 3));
-            }
-            *reinterpret_cast<uint2*>(row + e + skip) = make_uint2(w[0], w[1]);
-            hi = skip;
+        const int lane = threadIdx.x & 31, skip = 8 - off;  // skip codes lie before the boundary
+        const uint32_t all = __ballot_sync(0xffffffffu, whole);
+        uint32_t w[4] = {c.x, c.y, __shfl_down_sync(0xffffffffu, c.x, 1), __shfl_down_sync(0xffffffffu, c.y, 1)};
+        if (skip & 4) {
+            w[0] = w[1];
+            w[1] = w[2];
+            w[2] = w[3];
         }
-        if (with_prev) lo = 8 - off;
+        w[0] = __funnelshift_r(w[0], w[1], 8 * (skip & 3));
+        w[1] = __funnelshift_r(w[1], w[2], 8 * (skip & 3));
+        if (whole) {
+            if (lane < 31 && ((all >> (lane + 1)) & 1u)) {
+                *reinterpret_cast<uint2*>(p + skip) = make_uint2(w[0], w[1]);
+            } else {  // my last `off` codes alone
+                int8_t* t = p + skip;
+                uint32_t left = w[0];
+                if (off & 4) {
+                    *reinterpret_cast<uint32_t*>(t) = left;
+                    t += 4;
+                    left = w[1];
+                }
+                if (off & 2) {
+                    *reinterpret_cast<uint16_t*>(t) = (uint16_t)left;
+                    t += 2;
+                    left >>= 16;
+                }
+                if (off & 1) *t = (int8_t)left;
+            }
+            if (lane == 0 || !((all >> (lane - 1)) & 1u)) {  // my first `skip` codes alone
+                int8_t* t = p;
+                uint32_t lo = c.x, hi = c.y;
+                if (skip & 1) {
+                    *t++ = (int8_t)lo;
+                    lo = __funnelshift_r(lo, hi, 8);
+                    hi >>= 8;
+                }
+                if (skip & 2) {
+                    *reinterpret_cast<uint16_t*>(t) = (uint16_t)lo;
+                    t += 2;
+                    lo = __funnelshift_r(lo, hi, 16);
+                }
+                if (skip & 4) *reinterpret_cast<uint32_t*>(t) = lo;
+            }
+        }
     }
+    if (!whole) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i >= lo && i < hi && e + i >= 0 && e + i < K)
-            row[e + i] = (int8_t)((i < 4 ? c.x >> (8 * i) : c.y >> (8 * (i - 4))) & 0xFFu);
+        for (int i = 0; i < 8; ++i)
+            if (e + i >= 0 && e + i < K) p[i] = (int8_t)((i < 4 ? c.x >> (8 * i) : c.y >> (8 * (i - 4))) & 0xFFu);
+    }
 }
 
-// g / (1 + e^-g) * u, with the exponential of a number below zero so that
-// nothing overflows and the divisor stays in [1, 2].
+// g / (1 + e^-g) * u. For g below -88 the exponential is infinite and the
+// result zero (exactly, below 3e-37 * |u|).
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    const float t = __expf(-fabsf(g));
-    return g * __fdividef(g < 0.f ? t : 1.f, 1.f + t) * u;
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));  // within one unit; 0 for infinity
+    return g * r * u;
+}
+
+// max(m, |v|), NaN if either is.
+__device__ __forceinline__ float max_abs(float m, float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    return r;
 }
 
 __host__ __device__ constexpr bool two_inputs(int mode) { return mode == kRowNormResidual || mode == kRowSiluMul; }
 __host__ __device__ constexpr bool is_norm(int mode) { return mode == kRowNorm || mode == kRowNormResidual; }
 
-// From the inputs x and r of a group: v = y (h * gamma for the norms) in x's
-// place, the sum of squares of h, and h in r's place where there is a residual.
-template <class T, int MODE>
-__device__ __forceinline__ void combine(float* x, float* r, const float* gamma, float& ss) {
+// From the inputs x and r of a group: v = y (h * gamma for the norms), the sum
+// of squares of h, and h in x's place where there is a residual. The sum of two
+// 16-bit numbers is rounded once, as it would be from fp32.
+__device__ __forceinline__ void add_raw(Raw<__nv_bfloat16>& x, const Raw<__nv_bfloat16>& r) {
+    __nv_bfloat162* a = reinterpret_cast<__nv_bfloat162*>(x.w);
+    const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(r.w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (MODE == kRowNormResidual) x[i] = r[i] = to_float(from_float<T>(x[i] + r[i]));
-        if (MODE == kRowSiluMul) x[i] = silu_mul(x[i], r[i]);
-        if (is_norm(MODE)) {
-            ss = __fmaf_rn(x[i], x[i], ss);
-            x[i] *= gamma[i];
+    for (int i = 0; i < 4; ++i) a[i] = __hadd2_rn(a[i], b[i]);
+}
+__device__ __forceinline__ void add_raw(Raw<__half>& x, const Raw<__half>& r) {
+    __half2* a = reinterpret_cast<__half2*>(x.w);
+    const __half2* b = reinterpret_cast<const __half2*>(r.w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = __hadd2_rn(a[i], b[i]);
+}
+__device__ __forceinline__ void add_raw(Raw<float>& x, const Raw<float>& r) {
+    float* a = reinterpret_cast<float*>(x.w);
+    const float* b = reinterpret_cast<const float*>(r.w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] += b[i];
+}
+template <class T, int MODE>
+__device__ __forceinline__ void combine(Raw<T>& x, const Raw<T>& r, const float* gamma, float* v, float& ss) {
+    if (MODE == kRowNormResidual) add_raw(x, r);
+    unpack(x, v);
+    if (MODE == kRowSiluMul) {
+        float u[8];
+        unpack(r, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = silu_mul(v[i], u[i]);
+    }
+    if (is_norm(MODE)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            ss = __fmaf_rn(v[i], v[i], ss);
+            v[i] *= gamma[i];
         }
     }
 }
@@ -226,8 +282,9 @@ struct RowScale {
 // Reduces the row's maximum and sum over the blockDim.x threads that hold it,
 // and writes its scale. s: 64 words, another set for the row after this one.
 template <int MODE>
-__device__ __forceinline__ RowScale row_scale(const RowArgs& a, int64_t row, uint32_t top, float ss, uint32_t* s) {
-    top = __reduce_max_sync(0xffffffffu, top);
+__device__ __forceinline__ RowScale row_scale(const RowArgs& a, int64_t row, float largest, float ss, uint32_t* s) {
+    // as bits: ordered like the values, NaN above infinity
+    uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(largest));
     if (is_norm(MODE)) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -268,141 +325,136 @@ __device__ __forceinline__ RowScale row_scale(const RowArgs& a, int64_t row, uin
     if (threadIdx.x == 0) a.scale[row] = x.finite ? scale : __uint_as_float(0x7FC00000u);
     return x;
 }
-template <int MODE>
-__device__ __forceinline__ void look(float* v, uint32_t& top) {
+__device__ __forceinline__ void look(const float* v, float& top) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);  // NaN above infinity
+    for (int i = 0; i < 8; ++i) top = max_abs(top, v[i]);
+}
+// The same for a group as it lies in memory.
+__device__ __forceinline__ void look(const Raw<__nv_bfloat16>& x, float& top) {
+    const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(x.w);
+    __nv_bfloat162 m = __habs2(e[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, __habs2(e[i]));
+    top = max_abs(max_abs(top, __low2float(m)), __high2float(m));
+}
+__device__ __forceinline__ void look(const Raw<__half>& x, float& top) {
+    const __half2* e = reinterpret_cast<const __half2*>(x.w);
+    __half2 m = __habs2(e[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, __habs2(e[i]));
+    top = max_abs(max_abs(top, __low2float(m)), __high2float(m));
+}
+__device__ __forceinline__ void look(const Raw<float>& x, float& top) {
+    look(reinterpret_cast<const float*>(x.w), top);
 }
 template <int MODE>
 __device__ __forceinline__ uint2 codes_of(float* v, const RowScale& s) {
-    if (is_norm(MODE)) {
+    if (is_norm(MODE) && s.pre != 1.f) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= s.pre;
     }
     return codes8(v, s.inv, s.finite);
 }
 
-__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-// All but the latest `left` (at most 3) groups of this thread's copies have landed.
-__device__ __forceinline__ void wait_copies(int left) {
-    if (left >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
-    else if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
-constexpr int kMaxStages = 4;
-
 // blockDim.x threads per row (one warp, then blockDim.y rows at a time; or the
-// whole block), ITEMS groups each, `stages` rows ahead. EDGE: rows do not all
-// start on a 16-byte boundary (or end a whole group); x, r and ro lie at the same
-// offset from one. Otherwise they do, K % 8 == 0 and the codes' rows lie on 8-byte
-// boundaries.
-template <class T, int MODE, int ITEMS, bool EDGE>
-__global__ void __launch_bounds__(ITEMS == 1 || (ITEMS == 2 && sizeof(T) == 2) ? 1024 : 512)
-    rows_kernel(const RowArgs a, const int stages) {
-    extern __shared__ uint4 slots[];  // [stage][input][item][16 bytes of a group][thread]
+// whole block), ITEMS groups each. EDGE: rows do not all start on a 16-byte
+// boundary (or end a whole group); x, r and ro lie at the same offset from one.
+// Otherwise they do, K % 8 == 0 and the codes' rows lie on 8-byte boundaries.
+template <class T, int MODE, int ITEMS, bool EDGE, int THREADS>
+__global__ void __launch_bounds__(THREADS) rows_kernel(const RowArgs a) {
     __shared__ uint32_t s[2][64];
-    constexpr int kIn = two_inputs(MODE) ? 2 : 1, kW = (int)sizeof(T) / 2;
-    const int n = blockDim.x, all = n * blockDim.y;
-    uint4* mine = slots + threadIdx.y * n + threadIdx.x;
+    // quantisation needs the values twice, but never as fp32 at once
+    constexpr bool kPacked = MODE == kRowQuantize;
+    const int n = blockDim.x;
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // first element of this thread's group i of a row
+    // first element of this thread's group i of row m
     auto lead = [&](int64_t m) {
         return EDGE ? (int)(reinterpret_cast<uintptr_t>(static_cast<const T*>(a.x) + m * a.ldx) & 15u) / (int)sizeof(T) : 0;
     };
     auto group = [&](int i, int off) { return (i * n + (int)threadIdx.x) * 8 - off; };
     auto whole = [&](int e) { return EDGE ? e >= 0 && e + 8 <= a.K : e < a.K; };
-    auto fetch = [&](int64_t m, int st) {
-        if (m < a.M) {
-            const int off = lead(m);
+    auto piece = [&](const T* p, int e) {  // the elements of a group that lie in the row, zeros beside them
+        Raw<T> x;
+        T* v = reinterpret_cast<T*>(x.w);
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i) {
-                const int e = group(i, off);
-                if (!whole(e)) continue;
-#pragma unroll
-                for (int w = 0; w < kW; ++w) {
-                    copy16(mine + (((st * kIn + 0) * ITEMS + i) * kW + w) * all,
-                           reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + m * a.ldx + e) + w);
-                    if (kIn == 2)
-                        copy16(mine + (((st * kIn + 1) * ITEMS + i) * kW + w) * all,
-                               reinterpret_cast<const uint4*>(static_cast<const T*>(a.r) + m * a.ldr + e) + w);
-                }
-            }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        for (int k = 0; k < 8; ++k) v[k] = e + k >= 0 && e + k < a.K ? p[e + k] : from_float<T>(0.f);
+        return x;
     };
-    auto slot = [&](int st, int in, int i) {
-        Raw<T> r;
-#pragma unroll
-        for (int w = 0; w < kW; ++w) r.w[w] = mine[(((st * kIn + in) * ITEMS + i) * kW + w) * all];
-        return r;
-    };
-    for (int st = 0; st < stages; ++st) fetch(row + st * step, st);
-    Raw<T> gamma[ITEMS];
-    if (is_norm(MODE) && !EDGE) {
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i)
-            if (group(i, 0) < a.K) gamma[i] = load_raw(static_cast<const T*>(a.gamma) + group(i, 0));
-    }
-    int st = 0;
-    for (int turn = 0; row < a.M; row += step, turn ^= 1) {
-        const int off = lead(row);
-        float v[ITEMS][8], ss = 0.f;
-        uint32_t top = 0;
-        wait_copies(stages - 1);
+    Raw<T> x[ITEMS], r[two_inputs(MODE) ? ITEMS : 1];
+    auto fetch = [&](int64_t m) {
+        const T* px = static_cast<const T*>(a.x) + m * a.ldx;
+        const T* pr = static_cast<const T*>(a.r) + m * a.ldr;
+        const int off = lead(m);
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             const int e = group(i, off);
-            float o[8], g[8];
             if (whole(e)) {
-                unpack(slot(st, 0, i), v[i]);
-                if (kIn == 2) unpack(slot(st, 1, i), o);
-                if (is_norm(MODE)) {
+                x[i] = load_raw(px + e);
+                if constexpr (two_inputs(MODE)) r[i] = load_raw(pr + e);
+            } else if constexpr (EDGE) {
+                x[i] = piece(px, e);
+                if constexpr (two_inputs(MODE)) r[i] = piece(pr, e);
+            } else {
+                x[i] = {};
+                if constexpr (two_inputs(MODE)) r[i] = {};
+            }
+        }
+    };
+    if (row < a.M) fetch(row);
+    Raw<T> gamma[ITEMS];
+    if constexpr (is_norm(MODE) && !EDGE) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            gamma[i] = {};
+            if (group(i, 0) < a.K) gamma[i] = load_raw(static_cast<const T*>(a.gamma) + group(i, 0));
+        }
+    }
+    for (int turn = 0; row < a.M; row += step, turn ^= 1) {
+        const int off = lead(row);
+        float v[kPacked ? 1 : ITEMS][8], ss = 0.f, top = 0.f;
+        Raw<T> now[kPacked ? ITEMS : 1];
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            if constexpr (kPacked) {
+                now[i] = x[i];
+                look(x[i], top);
+            } else {
+                const int e = group(i, off);
+                float g[8];
+                if constexpr (is_norm(MODE)) {
                     if (EDGE) load_any(static_cast<const T*>(a.gamma), e, a.K, g);
                     else unpack(gamma[i], g);
                 }
-            } else if constexpr (!EDGE) {
-                continue;
-            } else {
+                combine<T, MODE>(x[i], r[two_inputs(MODE) ? i : 0], g, v[i], ss);
+                if constexpr (MODE == kRowNormResidual) {
+                    T* ro = static_cast<T*>(a.ro) + row * a.ldo + e;
+                    if (whole(e)) {
+                        *reinterpret_cast<Raw<T>*>(ro) = x[i];
+                    } else if (EDGE) {
+                        const T* h = reinterpret_cast<const T*>(x[i].w);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const bool in = e + k >= 0 && e + k < a.K;
-                    v[i][k] = in ? to_float(static_cast<const T*>(a.x)[row * a.ldx + e + k]) : 0.f;
-                    if (kIn == 2) o[k] = in ? to_float(static_cast<const T*>(a.r)[row * a.ldr + e + k]) : 0.f;
-                    if (is_norm(MODE)) g[k] = in ? to_float(static_cast<const T*>(a.gamma)[e + k]) : 0.f;
+                        for (int k = 0; k < 8; ++k)
+                            if (e + k >= 0 && e + k < a.K) ro[k] = h[k];
+                    }
                 }
+                look(v[i], top);
             }
-            combine<T, MODE>(v[i], o, g, ss);
-            if (MODE == kRowNormResidual) {
-                T* ro = static_cast<T*>(a.ro) + row * a.ldo + e;
-                if (whole(e)) {
-                    store_raw(ro, o);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (e + k >= 0 && e + k < a.K) ro[k] = from_float<T>(o[k]);
-                }
-            }
-            look<MODE>(v[i], top);
         }
+        if (row + step < a.M) fetch(row + step);
         const RowScale sc = row_scale<MODE>(a, row, top, ss, s[turn]);
-        // (every lane's reads of the slots are behind it: their values went into the reduction)
-        fetch(row + stages * step, st);
-        st = st + 1 == stages ? 0 : st + 1;
         int8_t* q = a.q + row * a.ldq;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             const int e = group(i, off);
-            if (EDGE) store_codes_any(q, e, a.K, codes_of<MODE>(v[i], sc));
-            else if (e < a.K) *reinterpret_cast<uint2*>(q + e) = codes_of<MODE>(v[i], sc);
+            if constexpr (kPacked) unpack(now[i], v[0]);
+            const uint2 c = codes_of<MODE>(v[kPacked ? 0 : i], sc);
+            if (EDGE) store_codes_any(q, e, a.K, c);
+            else if (e < a.K) *reinterpret_cast<uint2*>(q + e) = c;
         }
     }
-    wait_copies(0);
 }
 
 // Inputs at any alignment, in groups that lie on x's 16-byte boundaries.
@@ -422,24 +474,29 @@ __global__ void __launch_bounds__(512) rows_any_kernel(const RowArgs a) {
             float o[8], g[8];
             if (MODE == kRowNormResidual && again) {
                 load_any(static_cast<const T*>(a.ro) + row * a.ldo, e, a.K, v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = 0.f;
             } else {
                 load_any(xr, e, a.K, v);
                 if (two_inputs(MODE)) load_any(static_cast<const T*>(a.r) + row * a.ldr, e, a.K, o);
             }
             if (is_norm(MODE)) load_any(static_cast<const T*>(a.gamma), e, a.K, g);
-            combine<T, MODE>(v, o, g, ss);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (MODE == kRowNormResidual && !again) v[i] = o[i] = to_float(from_float<T>(v[i] + o[i]));
+                if (MODE == kRowSiluMul) v[i] = silu_mul(v[i], o[i]);
+                if (is_norm(MODE)) {
+                    ss = __fmaf_rn(v[i], v[i], ss);
+                    v[i] *= g[i];
+                }
+            }
             if (MODE == kRowNormResidual && !again) store_any(static_cast<T*>(a.ro) + row * a.ldo, e, a.K, o);
         };
-        float ss = 0.f;
-        uint32_t top = 0;
+        float ss = 0.f, top = 0.f;
         if constexpr (ITEMS > 0) {
             float v[ITEMS][8];
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
                 group((i * n + (int)threadIdx.x) * 8 - off, v[i], ss, false);
-                look<MODE>(v[i], top);
+                look(v[i], top);
             }
             const RowScale sc = row_scale<MODE>(a, row, top, ss, s[turn]);
 #pragma unroll
@@ -451,7 +508,7 @@ __global__ void __launch_bounds__(512) rows_any_kernel(const RowArgs a) {
             float v[8], unused = 0.f;
             for (int64_t e = (int64_t)threadIdx.x * 8; e < end; e += 8 * n) {
                 group((int)e - off, v, ss, false);
-                look<MODE>(v, top);
+                look(v, top);
             }
             const RowScale sc = row_scale<MODE>(a, row, top, ss, s[turn]);
             for (int64_t e = (int64_t)threadIdx.x * 8; e < end; e += 8 * n) {
@@ -465,11 +522,10 @@ __global__ void __launch_bounds__(512) rows_any_kernel(const RowArgs a) {
 // A launch whose set-up may overlap the stream's previous kernel (the kernels
 // wait for it before they touch memory).
 template <class... Params, class... Args>
-cudaError_t go(void (*kernel)(Params...), dim3 grid, dim3 block, int smem, cudaStream_t st, Args... args) {
+cudaError_t go(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -479,8 +535,7 @@ cudaError_t go(void (*kernel)(Params...), dim3 grid, dim3 block, int smem, cudaS
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Persistent blocks: as many as are resident without dynamic shared memory,
-// found once per kernel and block size (by warps per block).
+// Persistent blocks: as many as are resident, found once per kernel and block size (by warps per block).
 template <class... Params>
 cudaError_t resident(void (*kernel)(Params...), int threads, std::atomic<int>* known, int* per_sm) {
     int n = known[threads / 32].load(std::memory_order_relaxed);
@@ -494,33 +549,15 @@ cudaError_t resident(void (*kernel)(Params...), int threads, std::atomic<int>* k
     return cudaSuccess;
 }
 
-constexpr int kSlotBytes = 200 * 1024;  // shared memory of an SM's slots
-
-template <class T, int MODE, int ITEMS, bool EDGE>
-cudaError_t launch_slots(const RowArgs& a, dim3 block, int sms, cudaStream_t st) {
+template <class T, int MODE, int ITEMS, bool EDGE, int THREADS>
+cudaError_t launch_instance(const RowArgs& a, dim3 block, int sms, cudaStream_t st) {
     static std::atomic<int> known[33];
-    static std::atomic<bool> allowed[64];  // by device: more than 48 KB of shared memory
-    auto kernel = rows_kernel<T, MODE, ITEMS, EDGE>;
-    const int threads = (int)(block.x * block.y);
-    int dev = 0, per_sm = 1;
-    cudaError_t e = resident(kernel, threads, known, &per_sm);
-    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    auto kernel = rows_kernel<T, MODE, ITEMS, EDGE, THREADS>;
+    int per_sm = 1;
+    const cudaError_t e = resident(kernel, (int)(block.x * block.y), known, &per_sm);
     if (e != cudaSuccess) return e;
-    if (dev >= 64 || !allowed[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlotBytes);
-        if (e != cudaSuccess) return e;
-        if (dev < 64) allowed[dev].store(true, std::memory_order_relaxed);
-    }
-    const int bytes = threads * ITEMS * 8 * (int)sizeof(T) * (two_inputs(MODE) ? 2 : 1);  // of one stage
-    while (per_sm > 1 && per_sm * bytes > kSlotBytes) --per_sm;
     const int64_t rows = (a.M + block.y - 1) / block.y, most = (int64_t)sms * per_sm;
-    const unsigned grid = (unsigned)(rows < most ? rows : most);
-    // rows ahead: what fits, and no more than a block has
-    const int64_t turns = (rows + grid - 1) / grid;
-    int stages = kSlotBytes / (per_sm * bytes);
-    stages = stages < kMaxStages ? stages : kMaxStages;
-    stages = stages < turns ? stages : (int)turns;
-    return go(kernel, dim3(grid), block, stages * bytes, st, a, stages);
+    return go(kernel, dim3((unsigned)(rows < most ? rows : most)), block, st, a);
 }
 
 template <class T, int MODE, int ITEMS>
@@ -531,7 +568,7 @@ cudaError_t launch_any(const RowArgs& a, dim3 block, int sms, cudaStream_t st) {
     const cudaError_t e = resident(kernel, (int)(block.x * block.y), known, &per_sm);
     if (e != cudaSuccess) return e;
     const int64_t rows = (a.M + block.y - 1) / block.y, most = (int64_t)sms * per_sm;
-    return go(kernel, dim3((unsigned)(rows < most ? rows : most)), block, 0, st, a);
+    return go(kernel, dim3((unsigned)(rows < most ? rows : most)), block, st, a);
 }
 
 template <class T, int MODE>
@@ -550,34 +587,39 @@ cudaError_t launch_rows(const RowArgs& a, int sms, cudaStream_t st) {
     auto threads = [&](int items) { return (groups + items - 1) / items + 31 & ~(int64_t)31; };
     dim3 block(32, 1);
     int items = 0;
-    const int most2 = sizeof(T) == 2 ? 1024 : 512;
+    // Four groups a thread halve what a row's reduction costs each element, two
+    // leave room for more threads. Measured (bf16): norm 8192 x 5120 25.8 us with
+    // four, 30.6 with two; with residual 46.5 and 47.8; silu * up 4096 x 8192 32.7
+    // and 34.0, but 2048 x 13824 32.3 and 30.5 and fp32 41 and 35 (norm 4096 x 4096).
+    const bool four = sizeof(T) == 2 && threads(4) >= 64 && threads(4) <= 256;
     if (groups <= 64) {
         // a warp per row, eight rows per block
         items = groups <= 32 ? 1 : 2;
         block.y = (unsigned)(a.M < 8 ? a.M : 8);
-    } else if (threads(1) <= 1024 && a.M <= sms) {
+    } else if (threads(1) <= 512 && a.M <= sms) {
         items = 1;  // few rows: the shortest way through one
-    } else if (threads(2) <= most2) {
+    } else if (four) {
+        items = 4;
+    } else if (threads(2) <= (sizeof(T) == 2 ? 1024 : 512)) {
         items = 2;
     } else if (threads(4) <= 512) {
         items = 4;
     }
-    if (items > 0 && block.y == 1) block.x = groups <= 64 ? 32 : (unsigned)threads(items);
+    if (groups > 64 && items > 0) block.x = (unsigned)threads(items);
     if (items == 0 || !same) {
-        if (items == 0 || items == 4 || threads(2) > 512) {
-            block = dim3(512, 1);
-            return launch_any<T, MODE, 0>(a, block, sms, st);
-        }
-        if (block.x > 32) block.x = (unsigned)threads(2);
+        if (items == 0 || threads(2) > 512) return launch_any<T, MODE, 0>(a, dim3(512, 1), sms, st);
+        if (groups > 64) block.x = (unsigned)threads(2);
         return launch_any<T, MODE, 2>(a, block, sms, st);
     }
-    if (aligned)
-        return items == 1   ? launch_slots<T, MODE, 1, false>(a, block, sms, st)
-               : items == 2 ? launch_slots<T, MODE, 2, false>(a, block, sms, st)
-                            : launch_slots<T, MODE, 4, false>(a, block, sms, st);
-    return items == 1   ? launch_slots<T, MODE, 1, true>(a, block, sms, st)
-           : items == 2 ? launch_slots<T, MODE, 2, true>(a, block, sms, st)
-                        : launch_slots<T, MODE, 4, true>(a, block, sms, st);
+#define PATCH_ROWS(ITEMS, THREADS)                                                  \
+    (aligned ? launch_instance<T, MODE, ITEMS, false, THREADS>(a, block, sms, st) \
+             : launch_instance<T, MODE, ITEMS, true, THREADS>(a, block, sms, st))
+    if (items == 1) return PATCH_ROWS(1, 512);
+    if (items == 4) return PATCH_ROWS(4, 512);
+    if constexpr (sizeof(T) == 2)
+        if (block.x > 512) return PATCH_ROWS(2, 1024);
+    return PATCH_ROWS(2, 512);
+#undef PATCH_ROWS
 }
 
 template <class T>
@@ -655,7 +697,7 @@ cudaError_t launch_deq(const int8_t* q, int64_t ldq, const float* scale, int64_t
     const int64_t most = 2147483647ll / chunks * block.y;
     for (int64_t m0 = 0; m0 < M; m0 += most) {
         const int64_t rows = M - m0 < most ? M - m0 : most;
-        const cudaError_t e = go(dequantize_kernel<T>, dim3((unsigned)((rows + block.y - 1) / block.y * chunks)), block, 0, st,
+        const cudaError_t e = go(dequantize_kernel<T>, dim3((unsigned)((rows + block.y - 1) / block.y * chunks)), block, st,
                                  q + m0 * ldq, ldq, scale + m0, rows, K, chunks, out + m0 * ldo, ldo);
         if (e != cudaSuccess) return e;
     }
