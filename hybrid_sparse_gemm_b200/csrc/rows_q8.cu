@@ -16,9 +16,9 @@
 // their next row before they reduce the present one, so that loads stay in
 // flight across the barrier. For many rows the instructions count as much as
 // the bytes: about ten an element fill the issue slots that 6.5 TB/s leave.
-// Rows that do not lie on 16-byte boundaries are taken in groups that do (the
-// first and the last one partial); what lies at another offset is shifted into
-// place.
+// Rows that do not lie on 16-byte boundaries are taken in groups that do, with
+// the elements before the first and after the last group one to a lane; what
+// lies at another offset is shifted into place.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -153,64 +153,61 @@ __device__ __forceinline__ uint2 codes8(const float* v, float inv, bool finite) 
     }
     return make_uint2(w[0], w[1]);
 }
-// The codes of elements [e, e + 8) of a row of K, by a whole warp whose lanes
-// hold consecutive groups. Where the row of codes lies off the groups' 8-byte
-// boundaries, each lane stores the aligned word made of its last codes and the
-// next lane's first ones; a warp's outermost codes go in pieces of 4, 2 and 1,
-// and groups that are not whole byte by byte.
+// Codes off their rows' 8-byte boundaries by `off` (1..7): each lane stores the
+// aligned word made of the last `off` codes of its group c and the first ones of
+// the group after it (next); where there is none beside it, and before the
+// first group, the codes go in pieces of 4, 2 and 1. p: the group's first code.
+__device__ __forceinline__ void store_codes_off(int8_t* p, int off, uint2 c, uint2 next, bool has_prev, bool has_next) {
+    const int skip = 8 - off;  // codes before the boundary
+    uint32_t w[4] = {c.x, c.y, next.x, next.y};
+    if (skip & 4) {
+        w[0] = w[1];
+        w[1] = w[2];
+        w[2] = w[3];
+    }
+    w[0] = __funnelshift_r(w[0], w[1], 8 * (skip & 3));
+    w[1] = __funnelshift_r(w[1], w[2], 8 * (skip & 3));
+    if (has_next) {
+        *reinterpret_cast<uint2*>(p + skip) = make_uint2(w[0], w[1]);
+    } else {
+        int8_t* t = p + skip;
+        uint32_t left = w[0];
+        if (off & 4) {
+            *reinterpret_cast<uint32_t*>(t) = left;
+            t += 4;
+            left = w[1];
+        }
+        if (off & 2) {
+            *reinterpret_cast<uint16_t*>(t) = (uint16_t)left;
+            t += 2;
+            left >>= 16;
+        }
+        if (off & 1) *t = (int8_t)left;
+    }
+    if (!has_prev) {
+        int8_t* t = p;
+        uint32_t lo = c.x, hi = c.y;
+        if (skip & 1) {
+            *t++ = (int8_t)lo;
+            lo = __funnelshift_r(lo, hi, 8);
+            hi >>= 8;
+        }
+        if (skip & 2) {
+            *reinterpret_cast<uint16_t*>(t) = (uint16_t)lo;
+            t += 2;
+            lo = __funnelshift_r(lo, hi, 16);
+        }
+        if (skip & 4) *reinterpret_cast<uint32_t*>(t) = lo;
+    }
+}
+// The codes of elements [e, e + 8) of a row of K, wherever they lie.
 __device__ __forceinline__ void store_codes_any(int8_t* row, int e, int K, uint2 c) {
     int8_t* p = row + e;
-    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 7u);  // the same in a warp
-    const bool whole = e >= 0 && e + 8 <= K;
-    if (off == 0) {
-        if (whole) *reinterpret_cast<uint2*>(p) = c;
+    if (e >= 0 && e + 8 <= K) {
+        const int off = (int)(reinterpret_cast<uintptr_t>(p) & 7u);
+        if (off == 0) *reinterpret_cast<uint2*>(p) = c;
+        else store_codes_off(p, off, c, c, false, false);
     } else {
-        const int lane = threadIdx.x & 31, skip = 8 - off;  // skip codes lie before the boundary
-        const uint32_t all = __ballot_sync(0xffffffffu, whole);
-        uint32_t w[4] = {c.x, c.y, __shfl_down_sync(0xffffffffu, c.x, 1), __shfl_down_sync(0xffffffffu, c.y, 1)};
-        if (skip & 4) {
-            w[0] = w[1];
-            w[1] = w[2];
-            w[2] = w[3];
-        }
-        w[0] = __funnelshift_r(w[0], w[1], 8 * (skip & 3));
-        w[1] = __funnelshift_r(w[1], w[2], 8 * (skip & 3));
-        if (whole) {
-            if (lane < 31 && ((all >> (lane + 1)) & 1u)) {
-                *reinterpret_cast<uint2*>(p + skip) = make_uint2(w[0], w[1]);
-            } else {  // my last `off` codes alone
-                int8_t* t = p + skip;
-                uint32_t left = w[0];
-                if (off & 4) {
-                    *reinterpret_cast<uint32_t*>(t) = left;
-                    t += 4;
-                    left = w[1];
-                }
-                if (off & 2) {
-                    *reinterpret_cast<uint16_t*>(t) = (uint16_t)left;
-                    t += 2;
-                    left >>= 16;
-                }
-                if (off & 1) *t = (int8_t)left;
-            }
-            if (lane == 0 || !((all >> (lane - 1)) & 1u)) {  // my first `skip` codes alone
-                int8_t* t = p;
-                uint32_t lo = c.x, hi = c.y;
-                if (skip & 1) {
-                    *t++ = (int8_t)lo;
-                    lo = __funnelshift_r(lo, hi, 8);
-                    hi >>= 8;
-                }
-                if (skip & 2) {
-                    *reinterpret_cast<uint16_t*>(t) = (uint16_t)lo;
-                    t += 2;
-                    lo = __funnelshift_r(lo, hi, 16);
-                }
-                if (skip & 4) *reinterpret_cast<uint32_t*>(t) = lo;
-            }
-        }
-    }
-    if (!whole) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (e + i >= 0 && e + i < K) p[i] = (int8_t)((i < 4 ? c.x >> (8 * i) : c.y >> (8 * (i - 4))) & 0xFFu);
@@ -273,6 +270,19 @@ __device__ __forceinline__ void combine(Raw<T>& x, const Raw<T>& r, const float*
             v[i] *= gamma[i];
         }
     }
+}
+
+// The same for one element.
+template <class T, int MODE>
+__device__ __forceinline__ float combine_one(T& x, T r, T gamma, float& ss) {
+    if (MODE == kRowNormResidual) x = from_float<T>(to_float(x) + to_float(r));
+    float v = to_float(x);
+    if (MODE == kRowSiluMul) v = silu_mul(v, to_float(r));
+    if (is_norm(MODE)) {
+        ss = __fmaf_rn(v, v, ss);
+        v *= to_float(gamma);
+    }
+    return v;
 }
 
 struct RowScale {
@@ -357,10 +367,9 @@ __device__ __forceinline__ uint2 codes_of(float* v, const RowScale& s) {
 }
 
 // blockDim.x threads per row (one warp, then blockDim.y rows at a time; or the
-// whole block), ITEMS groups each. EDGE: rows do not all start on a 16-byte
-// boundary (or end a whole group); x, r and ro lie at the same offset from one.
-// Otherwise they do, K % 8 == 0 and the codes' rows lie on 8-byte boundaries.
-template <class T, int MODE, int ITEMS, bool EDGE, int THREADS>
+// whole block), ITEMS groups each. All rows on 16-byte boundaries (the codes' on
+// 8-byte ones), K % 8 == 0.
+template <class T, int MODE, int ITEMS, int THREADS>
 __global__ void __launch_bounds__(THREADS) rows_kernel(const RowArgs a) {
     __shared__ uint32_t s[2][64];
     // quantisation needs the values twice, but never as fp32 at once
@@ -370,50 +379,29 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const RowArgs a) {
     int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // first element of this thread's group i of row m
-    auto lead = [&](int64_t m) {
-        return EDGE ? (int)(reinterpret_cast<uintptr_t>(static_cast<const T*>(a.x) + m * a.ldx) & 15u) / (int)sizeof(T) : 0;
-    };
-    auto group = [&](int i, int off) { return (i * n + (int)threadIdx.x) * 8 - off; };
-    auto whole = [&](int e) { return EDGE ? e >= 0 && e + 8 <= a.K : e < a.K; };
-    auto piece = [&](const T* p, int e) {  // the elements of a group that lie in the row, zeros beside them
-        Raw<T> x;
-        T* v = reinterpret_cast<T*>(x.w);
+    auto group = [&](int i) { return (i * n + (int)threadIdx.x) * 8; };
+    Raw<T> x[ITEMS], r[two_inputs(MODE) ? ITEMS : 1], gamma[is_norm(MODE) ? ITEMS : 1];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = e + k >= 0 && e + k < a.K ? p[e + k] : from_float<T>(0.f);
-        return x;
-    };
-    Raw<T> x[ITEMS], r[two_inputs(MODE) ? ITEMS : 1];
+    for (int i = 0; i < ITEMS; ++i) {  // zeros past the row
+        x[i] = {};
+        if constexpr (two_inputs(MODE)) r[i] = {};
+        if constexpr (is_norm(MODE)) {
+            gamma[i] = {};
+            if (group(i) < a.K) gamma[i] = load_raw(static_cast<const T*>(a.gamma) + group(i));
+        }
+    }
     auto fetch = [&](int64_t m) {
         const T* px = static_cast<const T*>(a.x) + m * a.ldx;
         const T* pr = static_cast<const T*>(a.r) + m * a.ldr;
-        const int off = lead(m);
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const int e = group(i, off);
-            if (whole(e)) {
-                x[i] = load_raw(px + e);
-                if constexpr (two_inputs(MODE)) r[i] = load_raw(pr + e);
-            } else if constexpr (EDGE) {
-                x[i] = piece(px, e);
-                if constexpr (two_inputs(MODE)) r[i] = piece(pr, e);
-            } else {
-                x[i] = {};
-                if constexpr (two_inputs(MODE)) r[i] = {};
+        for (int i = 0; i < ITEMS; ++i)
+            if (group(i) < a.K) {
+                x[i] = load_raw(px + group(i));
+                if constexpr (two_inputs(MODE)) r[i] = load_raw(pr + group(i));
             }
-        }
     };
     if (row < a.M) fetch(row);
-    Raw<T> gamma[ITEMS];
-    if constexpr (is_norm(MODE) && !EDGE) {
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            gamma[i] = {};
-            if (group(i, 0) < a.K) gamma[i] = load_raw(static_cast<const T*>(a.gamma) + group(i, 0));
-        }
-    }
     for (int turn = 0; row < a.M; row += step, turn ^= 1) {
-        const int off = lead(row);
         float v[kPacked ? 1 : ITEMS][8], ss = 0.f, top = 0.f;
         Raw<T> now[kPacked ? ITEMS : 1];
 #pragma unroll
@@ -422,25 +410,13 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const RowArgs a) {
                 now[i] = x[i];
                 look(x[i], top);
             } else {
-                const int e = group(i, off);
                 float g[8];
-                if constexpr (is_norm(MODE)) {
-                    if (EDGE) load_any(static_cast<const T*>(a.gamma), e, a.K, g);
-                    else unpack(gamma[i], g);
-                }
+                if constexpr (is_norm(MODE)) unpack(gamma[i], g);
                 combine<T, MODE>(x[i], r[two_inputs(MODE) ? i : 0], g, v[i], ss);
-                if constexpr (MODE == kRowNormResidual) {
-                    T* ro = static_cast<T*>(a.ro) + row * a.ldo + e;
-                    if (whole(e)) {
-                        *reinterpret_cast<Raw<T>*>(ro) = x[i];
-                    } else if (EDGE) {
-                        const T* h = reinterpret_cast<const T*>(x[i].w);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (e + k >= 0 && e + k < a.K) ro[k] = h[k];
-                    }
-                }
+                if (MODE == kRowNormResidual && group(i) < a.K)
+                    *reinterpret_cast<Raw<T>*>(static_cast<T*>(a.ro) + row * a.ldo + group(i)) = x[i];
                 look(v[i], top);
+                // (h stays in x past the row: zeros, as they were)
             }
         }
         if (row + step < a.M) fetch(row + step);
@@ -448,11 +424,142 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const RowArgs a) {
         int8_t* q = a.q + row * a.ldq;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const int e = group(i, off);
             if constexpr (kPacked) unpack(now[i], v[0]);
             const uint2 c = codes_of<MODE>(v[kPacked ? 0 : i], sc);
-            if (EDGE) store_codes_any(q, e, a.K, c);
-            else if (e < a.K) *reinterpret_cast<uint2*>(q + e) = c;
+            if (group(i) < a.K) *reinterpret_cast<uint2*>(q + group(i)) = c;
+        }
+    }
+}
+
+// The same for rows at any alignment; x, r and ro lie at the same offset from a
+// 16-byte boundary. A warp's groups are consecutive. gamma's copy in shared
+// memory: it lies at another offset from the groups in every row.
+template <class T, int MODE, int ITEMS, int THREADS>
+__global__ void __launch_bounds__(THREADS) rows_edge_kernel(const RowArgs a) {
+    __shared__ uint32_t s[2][64];
+    extern __shared__ uint4 copy_of_gamma[];
+    T* gamma = reinterpret_cast<T*>(copy_of_gamma);
+    constexpr bool kPacked = MODE == kRowQuantize;
+    const int lane = threadIdx.x & 31;
+    const int first = ((int)threadIdx.x >> 5) * 32 * ITEMS + lane;  // this thread's first group
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // elements before the first group, groups, and this lane's element beside them (-1: none)
+    struct Split {
+        int head, groups, beside;
+    };
+    auto split = [&](int64_t m) {
+        Split p;
+        const int mis = (int)(reinterpret_cast<uintptr_t>(static_cast<const T*>(a.x) + m * a.ldx) & 15u);
+        p.head = min(a.K, (16 - mis) % 16 / (int)sizeof(T));
+        p.groups = (a.K - p.head) / 8;
+        const int tail = a.K - p.head - 8 * p.groups, t = (int)threadIdx.x;
+        p.beside = t < p.head ? t : t >= 8 && t < 8 + tail ? a.K - tail + t - 8 : -1;
+        return p;
+    };
+    Raw<T> x[ITEMS], r[two_inputs(MODE) ? ITEMS : 1];
+    T bx = from_float<T>(0.f), br = bx;  // the element beside the groups
+    auto fetch = [&](int64_t m) {
+        const Split p = split(m);
+        const T* px = static_cast<const T*>(a.x) + m * a.ldx;
+        const T* pr = static_cast<const T*>(a.r) + m * a.ldr;
+        if (p.beside >= 0) {
+            bx = px[p.beside];
+            if (two_inputs(MODE)) br = pr[p.beside];
+        }
+        px += p.head;
+        pr += p.head;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int g = first + 32 * i;
+            if (g < p.groups) {
+                x[i] = load_raw(px + 8 * g);
+                if constexpr (two_inputs(MODE)) r[i] = load_raw(pr + 8 * g);
+            } else {
+                x[i] = {};
+                if constexpr (two_inputs(MODE)) r[i] = {};
+            }
+        }
+    };
+    if (row < a.M) fetch(row);
+    if constexpr (is_norm(MODE)) {
+        const int all = blockDim.x * blockDim.y, t = threadIdx.y * blockDim.x + threadIdx.x;
+        for (int k = t; k < a.K; k += all) gamma[k] = static_cast<const T*>(a.gamma)[k];
+        __syncthreads();
+    }
+    for (int turn = 0; row < a.M; row += step, turn ^= 1) {
+        const Split p = split(row);
+        float v[kPacked ? 1 : ITEMS][8], ss = 0.f, top = 0.f, bv = 0.f;
+        Raw<T> now[kPacked ? ITEMS : 1];
+        T* ro = static_cast<T*>(a.ro) + row * a.ldo;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            if constexpr (kPacked) {
+                now[i] = x[i];
+                look(x[i], top);
+            } else {
+                const int g = first + 32 * i, e = p.head + 8 * g;
+                float y[8];
+                if constexpr (is_norm(MODE)) {
+                    if (g < p.groups) {
+                        // two boundaries' worth (the copy has room behind it), shifted
+                        constexpr int kWords = 2 * (int)sizeof(T);
+                        __align__(16) uint32_t w[kWords + 4];
+                        const int at = e * (int)sizeof(T);
+#pragma unroll
+                        for (int k = 0; k < kWords / 4 + 1; ++k)
+                            reinterpret_cast<uint4*>(w)[k] = copy_of_gamma[at / 16 + k];
+                        shift_down<kWords>(w, at & 15);
+                        const T* z = reinterpret_cast<const T*>(w);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) y[k] = to_float(z[k]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) y[k] = 0.f;
+                    }
+                }
+                combine<T, MODE>(x[i], r[two_inputs(MODE) ? i : 0], y, v[i], ss);
+                if (MODE == kRowNormResidual && g < p.groups) *reinterpret_cast<Raw<T>*>(ro + e) = x[i];
+                look(v[i], top);
+            }
+        }
+        if (p.beside >= 0) {
+            bv = combine_one<T, MODE>(bx, br, is_norm(MODE) ? gamma[p.beside] : bx, ss);
+            if (MODE == kRowNormResidual) ro[p.beside] = bx;
+            top = max_abs(top, bv);
+        }
+        if (row + step < a.M) fetch(row + step);
+        const RowScale sc = row_scale<MODE>(a, row, top, ss, s[turn]);
+        int8_t* q = a.q + row * a.ldq + p.head;
+        const int off = (int)(reinterpret_cast<uintptr_t>(q) & 7u);  // of every group
+        uint2 c[ITEMS];
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            if constexpr (kPacked) unpack(now[i], v[0]);
+            c[i] = codes_of<MODE>(v[kPacked ? 0 : i], sc);
+        }
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int g = first + 32 * i;
+            if (off == 0) {
+                if (g < p.groups) *reinterpret_cast<uint2*>(q + 8 * g) = c[i];
+            } else {
+                // the next group: the next lane's, or the first lane's next
+                const bool wrap = lane == 0 && i + 1 < ITEMS;
+                const uint2 give = wrap ? c[i + 1 < ITEMS ? i + 1 : i] : c[i];
+                uint2 next;
+                next.x = __shfl_sync(0xffffffffu, give.x, lane + 1);
+                next.y = __shfl_sync(0xffffffffu, give.y, lane + 1);
+                const bool has_next = g + 1 < p.groups && (lane < 31 || i + 1 < ITEMS);
+                const bool has_prev = g > 0 && (lane > 0 || i > 0);
+                if (g < p.groups) store_codes_off(q + 8 * g, off, c[i], next, has_prev, has_next);
+            }
+        }
+        if (p.beside >= 0) {
+            if (is_norm(MODE) && sc.pre != 1.f) bv *= sc.pre;
+            a.q[row * a.ldq + p.beside] = sc.finite ? (int8_t)(code_bits(bv, sc.inv) & 0xFFu) : (int8_t)0;
         }
     }
 }
@@ -522,10 +629,11 @@ __global__ void __launch_bounds__(512) rows_any_kernel(const RowArgs a) {
 // A launch whose set-up may overlap the stream's previous kernel (the kernels
 // wait for it before they touch memory).
 template <class... Params, class... Args>
-cudaError_t go(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t st, Args... args) {
+cudaError_t go(void (*kernel)(Params...), dim3 grid, dim3 block, int smem, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -549,15 +657,25 @@ cudaError_t resident(void (*kernel)(Params...), int threads, std::atomic<int>* k
     return cudaSuccess;
 }
 
+constexpr int kGammaBytes = 200 * 1024;  // of an SM's shared memory for the blocks' copies of gamma
+
 template <class T, int MODE, int ITEMS, bool EDGE, int THREADS>
 cudaError_t launch_instance(const RowArgs& a, dim3 block, int sms, cudaStream_t st) {
     static std::atomic<int> known[33];
-    auto kernel = rows_kernel<T, MODE, ITEMS, EDGE, THREADS>;
+    void (*kernel)(RowArgs);
+    if constexpr (EDGE) kernel = rows_edge_kernel<T, MODE, ITEMS, THREADS>;
+    else kernel = rows_kernel<T, MODE, ITEMS, THREADS>;
     int per_sm = 1;
     const cudaError_t e = resident(kernel, (int)(block.x * block.y), known, &per_sm);
     if (e != cudaSuccess) return e;
+    // gamma's copy, and room for the words read behind it
+    int smem = 0;
+    if constexpr (EDGE && is_norm(MODE)) {
+        smem = (a.K * (int)sizeof(T) + 15) / 16 * 16 + 32;
+        if (per_sm > kGammaBytes / smem) per_sm = kGammaBytes / smem;
+    }
     const int64_t rows = (a.M + block.y - 1) / block.y, most = (int64_t)sms * per_sm;
-    return go(kernel, dim3((unsigned)(rows < most ? rows : most)), block, st, a);
+    return go(kernel, dim3((unsigned)(rows < most ? rows : most)), block, smem, st, a);
 }
 
 template <class T, int MODE, int ITEMS>
@@ -568,7 +686,7 @@ cudaError_t launch_any(const RowArgs& a, dim3 block, int sms, cudaStream_t st) {
     const cudaError_t e = resident(kernel, (int)(block.x * block.y), known, &per_sm);
     if (e != cudaSuccess) return e;
     const int64_t rows = (a.M + block.y - 1) / block.y, most = (int64_t)sms * per_sm;
-    return go(kernel, dim3((unsigned)(rows < most ? rows : most)), block, st, a);
+    return go(kernel, dim3((unsigned)(rows < most ? rows : most)), block, 0, st, a);
 }
 
 template <class T, int MODE>
@@ -582,16 +700,18 @@ cudaError_t launch_rows(const RowArgs& a, int sms, cudaStream_t st) {
     const bool same = with_x(a.r, a.ldr) && with_x(a.ro, a.ldo);
     const bool aligned = same && a.K % 8 == 0 && ((at(a.x) | pitch(a.ldx) | at(a.gamma)) & 15u) == 0 &&
                          ((at(a.q) | (uintptr_t)a.ldq) & 7u) == 0;
-    // groups of eight in a row, one more where the first may be partial
-    const int64_t groups = aligned ? a.K / 8 : ((int64_t)a.K + 7) / 8 + 1;
+    const int64_t groups = (a.K + 7) / 8;  // of eight elements in a row
+    // gamma's copy has to fit what a block may use without asking
+    const bool edge = same && !(is_norm(MODE) && (int64_t)a.K * (int)sizeof(T) > 47 * 1024);
     auto threads = [&](int items) { return (groups + items - 1) / items + 31 & ~(int64_t)31; };
     dim3 block(32, 1);
     int items = 0;
     // Four groups a thread halve what a row's reduction costs each element, two
-    // leave room for more threads. Measured (bf16): norm 8192 x 5120 25.8 us with
-    // four, 30.6 with two; with residual 46.5 and 47.8; silu * up 4096 x 8192 32.7
-    // and 34.0, but 2048 x 13824 32.3 and 30.5 and fp32 41 and 35 (norm 4096 x 4096).
-    const bool four = sizeof(T) == 2 && threads(4) >= 64 && threads(4) <= 256;
+    // leave room for more threads. Measured (bf16, us with four and with two): norm
+    // 8192 x 5120 25.2 and 30.6, with residual 47 and 47.8, silu * up 4096 x 8192 32
+    // and 34, but 2048 x 13824 32.3 and 30.1; off the boundaries 2048 x 13823 36
+    // and 43. fp32 (norm and residual, 4096 x 4096): 41 and 35.
+    const bool four = sizeof(T) == 2 && threads(4) >= 64 && threads(4) <= (aligned ? 256 : 512);
     if (groups <= 64) {
         // a warp per row, eight rows per block
         items = groups <= 32 ? 1 : 2;
@@ -606,9 +726,11 @@ cudaError_t launch_rows(const RowArgs& a, int sms, cudaStream_t st) {
         items = 4;
     }
     if (groups > 64 && items > 0) block.x = (unsigned)threads(items);
-    if (items == 0 || !same) {
-        if (items == 0 || threads(2) > 512) return launch_any<T, MODE, 0>(a, dim3(512, 1), sms, st);
-        if (groups > 64) block.x = (unsigned)threads(2);
+    if (items == 0 || !(aligned || edge)) {
+        // (groups on x's boundaries: one more, where the first is partial)
+        const int64_t two = (groups + 2) / 2 + 31 & ~(int64_t)31;
+        if (items == 0 || two > 512) return launch_any<T, MODE, 0>(a, dim3(512, 1), sms, st);
+        if (two > 32) block = dim3((unsigned)two, 1);
         return launch_any<T, MODE, 2>(a, block, sms, st);
     }
 #define PATCH_ROWS(ITEMS, THREADS)                                                  \
@@ -697,7 +819,7 @@ cudaError_t launch_deq(const int8_t* q, int64_t ldq, const float* scale, int64_t
     const int64_t most = 2147483647ll / chunks * block.y;
     for (int64_t m0 = 0; m0 < M; m0 += most) {
         const int64_t rows = M - m0 < most ? M - m0 : most;
-        const cudaError_t e = go(dequantize_kernel<T>, dim3((unsigned)((rows + block.y - 1) / block.y * chunks)), block, st,
+        const cudaError_t e = go(dequantize_kernel<T>, dim3((unsigned)((rows + block.y - 1) / block.y * chunks)), block, 0, st,
                                  q + m0 * ldq, ldq, scale + m0, rows, K, chunks, out + m0 * ldo, ldo);
         if (e != cudaSuccess) return e;
     }
