@@ -986,6 +986,29 @@ struct Q8Call {
     int64_t pitch_y(int l, int64_t N) const { return ldy ? ldy[l] : N; }
 };
 
+// Parts of K of the split-K kernel, at least a slab each: the least of an
+// estimate in us, fitted to calls of 512 to 11008 rows, 2048 to 11008 columns and
+// 1 to 100 tokens with every P (within 8 % of the best P in all of them). Slabs
+// follow one another at 0.25 us in a CTA, a wave of CTAs costs 1 us more (95 % of
+// the slots fill: a cluster stays within a GPC), and every CTA takes 5 ns, and
+// 0.16 ns a token for its sums, of the whole GPU.
+int q8_parts(int64_t units, int kb_min, int kb_max, int tokens, int slots, double* us) {
+    double best = 1e300;
+    int parts = 1;
+    for (int p = 1; p <= std::min(kQ8MaxParts, kb_min); ++p) {
+        const int64_t at_once = std::max(1, (int)(0.95 * slots / p));
+        const double waves = (double)((units + at_once - 1) / at_once);
+        const double cost =
+            waves * (0.25 * ((kb_max + p - 1) / p) + 1.0) + (double)(units * p) * (0.005 + 0.00016 * tokens);
+        if (cost < best) {
+            best = cost;
+            parts = p;
+        }
+    }
+    *us = best;
+    return parts;
+}
+
 template <int G>
 patch_status run_q8_split(patch_group g, const Q8Call& c, int path, cudaStream_t st) {
     const int bn = path == PATCH_PATH_GEMM_SINGLE ? kGemmBN : c.M <= kDecodeBN ? kDecodeBN : kDecodeWideBN;
@@ -999,7 +1022,7 @@ patch_status run_q8_split(patch_group g, const Q8Call& c, int path, cudaStream_t
     a.n = g->n;
     a.status = g->status_dev;
     int64_t units = 0;
-    int kb = 8;
+    int kb_min = INT32_MAX, kb_max = 0;
     for (int l = 0; l < g->n; ++l) {
         patch_handle h = g->h[l];
         patch_status s = encode_codes(&maps.x[l], c.X[l], h->K, c.M, c.pitch_x(l, h->K), a.n_tok);
@@ -1017,11 +1040,11 @@ patch_status run_q8_split(patch_group g, const Q8Call& c, int path, cudaStream_t
         units += (int64_t)h->plan.S * a.MB;
         if (units > INT32_MAX / 8)
             return fail(PATCH_ERR_SHAPE, "M=%lld gives more than %d output tiles", (long long)c.M, INT32_MAX / 8);
-        kb = std::min(kb, h->plan.KB);
+        kb_min = std::min(kb_min, h->plan.KB);
+        kb_max = std::max(kb_max, h->plan.KB);
     }
-    // Parts of K: as many as keep every CTA resident (two per SM), at least one slab each.
-    a.P = 8;
-    while (a.P > 1 && (units * a.P > 4 * (int64_t)g->dev.sms || a.P > kb)) a.P /= 2;
+    double us;
+    a.P = q8_parts(units, kb_min, kb_max, std::min(a.M, a.n_tok), q8_split_ctas(bn) * g->dev.sms, &us);
     const cudaError_t e = launch_q8_split<G>(maps, a, bn, c.y_type, (int)units * a.P, st);
     if (e != cudaSuccess) return cuda_fail(e, "8-bit kernel launch");
     return PATCH_OK;

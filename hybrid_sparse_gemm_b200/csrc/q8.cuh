@@ -74,6 +74,8 @@ struct Q8SplitArgs {
 template <int G>
 cudaError_t launch_q8_split(const Q8Maps<G>& maps, const Q8SplitArgs<G>& a, int bn, int y_type, int grid,
                             cudaStream_t st);
+constexpr int kQ8MaxParts = 8;
+int q8_split_ctas(int bn);  // CTAs resident per SM
 cudaError_t q8_prepare_split();
 
 // Kernel on CTA pairs with two strips per CTA (many tokens). A work unit is

@@ -41,7 +41,7 @@ template <int BN, int STAGES, int CTAS>
 struct Cfg {
     static constexpr int kStage = kStageA + BN * 128;
     static constexpr int kSmemData = STAGES * kStage;
-    static constexpr int kSmemBytes = kSmemData + 1024 /*align*/ + 256 /*barriers*/;
+    static constexpr int kSmemBytes = kSmemData + 1024 /*align*/ + 256 /*barriers*/ + (BN + kStrip) * 4 /*scales*/;
     static constexpr int kTmemCols = BN + 4 <= 32 ? 32 : BN + 4 <= 64 ? 64 : BN + 4 <= 128 ? 128 : 256;
     static_assert(kStage % 1024 == 0, "stages keep the 1024-byte swizzle alignment");
     static_assert(BN * 128 * 4 <= kSmemData, "the partial sums fit in the stages");
@@ -71,6 +71,36 @@ __device__ __forceinline__ void store4(__half* p, float4 v) {
 }
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 
+// This CTA's share of a unit's items (int4 at the same place in every CTA of the
+// cluster): their sums over the P CTAs, handed to store().
+template <int P, class Store>
+__device__ __forceinline__ void join(uint32_t base, int rank, int items, Store store) {
+    constexpr int kAtOnce = P <= 4 ? 8 / P : 1;  // eight reads under way at a time
+    uint32_t from[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) from[p] = map_to_rank(base, p);
+    for (int i0 = rank * kThreads + (int)threadIdx.x; i0 < items; i0 += kAtOnce * P * kThreads) {
+        int4 v[kAtOnce][P];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int i = i0 + k * P * kThreads;
+            if (i < items)
+#pragma unroll
+                for (int p = 0; p < P; ++p) v[k][p] = ld_cluster(from[p] + (uint32_t)i * 16u);
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int i = i0 + k * P * kThreads;
+            if (i >= items) continue;
+            int4 sum = v[k][0];
+#pragma unroll
+            for (int p = 1; p < P; ++p)
+                sum = make_int4(sum.x + v[k][p].x, sum.y + v[k][p].y, sum.z + v[k][p].z, sum.w + v[k][p].w);
+            store(i, sum);
+        }
+    }
+}
+
 template <int BN, int STAGES, int CTAS, int G, class T>
 __global__ void __launch_bounds__(kThreads, CTAS)
     q8_split_kernel(const __grid_constant__ Q8Maps<G> maps, const __grid_constant__ Q8SplitArgs<G> a) {
@@ -84,6 +114,8 @@ __global__ void __launch_bounds__(kThreads, CTAS)
     int* kind = reinterpret_cast<int*>(acc_full + 1);  // [STAGES] 1: the stage's slab is 2:4
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kind + STAGES);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    float* s_sw = reinterpret_cast<float*>(smem + C::kSmemData + 256);  // [kStrip] the rows' scales
+    float* s_sx = s_sw + kStrip;                                        // [BN] the tokens' scales
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -208,6 +240,11 @@ __global__ void __launch_bounds__(kThreads, CTAS)
         asm volatile("griddepcontrol.wait;" ::: "memory");
         const int q = warp & 3;  // TMEM lane quadrant this warp may access
         const int tokens = min(a.n_tok, a.M - m0);
+        {
+            const int t = (int)threadIdx.x - 64;
+            s_sw[t] = L.w_scale[s * kStrip + t];
+            if (t < tokens) s_sx[t] = L.x_scale[m0 + t];
+        }
         int* part = reinterpret_cast<int*>(smem) + q * 32 + lane;  // [token][row]
         bool ok = mbar_try_wait(acc_full, 0);
         const uint64_t t0 = globaltimer();
@@ -239,24 +276,29 @@ __global__ void __launch_bounds__(kThreads, CTAS)
     }
     const int items = min(a.n_tok, a.M - m0) * (kStrip / 4);
     T* y0 = static_cast<T*>(L.Y) + (int64_t)m0 * L.ldy + (int64_t)s * kStrip;
-    for (int i = rank * kThreads + (int)threadIdx.x; i < items; i += P * kThreads) {
+    auto store = [&](int i, int4 sum) {
         const int tok = i / (kStrip / 4), row = (i % (kStrip / 4)) * 4;
-        const float sx = L.x_scale[m0 + tok];
-        const float4 sw = *reinterpret_cast<const float4*>(L.w_scale + s * kStrip + row);
-        const uint32_t at = smem_u32(smem) + (uint32_t)i * 16u;
-        int4 sum;
-        if (P == 1) {
-            sum = *reinterpret_cast<const int4*>(smem + (size_t)i * 16);
-        } else {
-            int4 v[8];
-#pragma unroll
-            for (int p = 0; p < 8; ++p) v[p] = p < P ? ld_cluster(map_to_rank(at, p)) : make_int4(0, 0, 0, 0);
-            sum = v[0];
-#pragma unroll
-            for (int p = 1; p < 8; ++p) sum = make_int4(sum.x + v[p].x, sum.y + v[p].y, sum.z + v[p].z, sum.w + v[p].w);
-        }
+        const float sx = s_sx[tok];
+        const float4 sw = *reinterpret_cast<const float4*>(s_sw + row);
         store4(y0 + tok * L.ldy + row, make_float4((float)sum.x * sx * sw.x, (float)sum.y * sx * sw.y,
                                                    (float)sum.z * sx * sw.z, (float)sum.w * sx * sw.w));
+    };
+    if (P == 1) {
+#pragma unroll 4
+        for (int i = (int)threadIdx.x; i < items; i += kThreads)
+            store(i, *reinterpret_cast<const int4*>(smem + (size_t)i * 16));
+    } else {
+        // (one CTA draws about 20 bytes a cycle from the others)
+        const uint32_t base = smem_u32(smem);
+        switch (P) {
+            case 2: join<2>(base, rank, items, store); break;
+            case 3: join<3>(base, rank, items, store); break;
+            case 4: join<4>(base, rank, items, store); break;
+            case 5: join<5>(base, rank, items, store); break;
+            case 6: join<6>(base, rank, items, store); break;
+            case 7: join<7>(base, rank, items, store); break;
+            default: join<8>(base, rank, items, store); break;
+        }
     }
     if (P > 1) cluster_sync();  // no CTA leaves while another may still read its sums
 }
@@ -286,8 +328,11 @@ cudaError_t launch(const Q8Maps<G>& maps, const Q8SplitArgs<G>& a, int grid, cud
     return cudaLaunchKernelEx(&cfg, q8_split_kernel<BN, STAGES, CTAS, G, T>, maps, a);
 }
 
-// BN tokens per unit; stages and resident CTAs share the SM's shared memory.
-#define Q8_SPLIT_CONFIGS(X) X(16, 6, 2) X(64, 4, 2) X(128, 3, 2)
+// BN tokens per unit; stages and resident CTAs share the SM's shared memory. More
+// CTAs keep more slabs in flight, but each joins and stores sums. Measured at 4096
+// x 4096 (2:4 tiles 70 %): one token 4.7 us with 3 stages x 4 CTAs, 5.4 with 6 x 2;
+// 64 tokens 6.7 us with 4 x 2, 7.3 with 3 x 3.
+#define Q8_SPLIT_CONFIGS(X) X(16, 3, 4) X(64, 4, 2) X(128, 3, 2)
 
 template <int BN, int STAGES, int CTAS>
 cudaError_t prepare_all() {
@@ -302,6 +347,14 @@ cudaError_t prepare_all() {
 }
 
 }  // namespace
+
+int q8_split_ctas(int bn) {
+#define Q8_CTAS(BN, STAGES, CTAS) \
+    if (bn == BN) return CTAS;
+    Q8_SPLIT_CONFIGS(Q8_CTAS)
+#undef Q8_CTAS
+    return 1;
+}
 
 cudaError_t q8_prepare_split() {
     cudaError_t e = cudaSuccess;
