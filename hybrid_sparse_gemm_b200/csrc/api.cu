@@ -953,39 +953,6 @@ patch_status run_group(patch_group g, const void* const* X, int64_t M, void* con
     return PATCH_OK;
 }
 
-// The kernel an 8-bit call runs: the split-K kernel with 16- or 64-token units
-// (GEMV, M <= 64) or with 128-token units (GEMM_SINGLE, any M), or CTA pairs
-// with two strips per CTA (GEMM_WIDE, any M).
-patch_status resolve_path_q8(patch_group g, int path, int64_t M, int* out) {
-    if (path == PATCH_PATH_AUTO) path = M <= kDecodeWideBN ? PATCH_PATH_GEMV : PATCH_PATH_GEMM;
-    if (path == PATCH_PATH_GEMM) {
-        int64_t quads = 0;
-        for (int l = 0; l < g->n; ++l) quads += (g->h[l]->plan.S + 3) / 4;
-        path = quads * ((M + kQ8WideBN - 1) / kQ8WideBN) >= g->dev.q8_wide_clusters ? PATCH_PATH_GEMM_WIDE
-                                                                                   : PATCH_PATH_GEMM_SINGLE;
-    }
-    if (path != PATCH_PATH_GEMV && path != PATCH_PATH_GEMM_SINGLE && path != PATCH_PATH_GEMM_WIDE)
-        return fail(PATCH_ERR_UNSUPPORTED, "path %d has no 8-bit kernel", path);
-    if (path == PATCH_PATH_GEMV && M > kDecodeWideBN)
-        return fail(PATCH_ERR_SHAPE, "the decode kernel takes M <= %d (got %lld)", kDecodeWideBN, (long long)M);
-    *out = path;
-    return PATCH_OK;
-}
-
-// The operands of an 8-bit call, one entry per member.
-struct Q8Call {
-    const int8_t* const* X;
-    const int64_t* ldx;           // NULL: contiguous
-    const float* const* x_scale;
-    int64_t M;
-    void* const* Y;
-    const int64_t* ldy;           // NULL: contiguous
-    int y_type;
-    // a single row needs no pitch, but its tensor map wants a multiple of 16 bytes
-    int64_t pitch_x(int l, int64_t K) const { return M == 1 ? (K + 15) & ~(int64_t)15 : ldx ? ldx[l] : K; }
-    int64_t pitch_y(int l, int64_t N) const { return ldy ? ldy[l] : N; }
-};
-
 // Parts of K of the split-K kernel, at least a slab each: the least of an
 // estimate in us, fitted to calls of 512 to 11008 rows, 2048 to 11008 columns and
 // 1 to 100 tokens with every P (within 8 % of the best P in all of them). Slabs
@@ -1009,20 +976,89 @@ int q8_parts(int64_t units, int kb_min, int kb_max, int tokens, int slots, doubl
     return parts;
 }
 
+// How the split-K kernel cuts a call: bn tokens per unit at most, mb tiles of
+// n_tok tokens (equal ones, a multiple of 16), P parts of K.
+struct Q8Split {
+    int bn, mb, n_tok, P;
+    int64_t units;
+    double us;  // estimate
+};
+Q8Split q8_split_plan(patch_group g, int bn, int64_t M) {
+    Q8Split x;
+    x.bn = bn;
+    const int64_t mb = (M + bn - 1) / bn;
+    x.n_tok = (int)(((M + mb - 1) / mb + 15) & ~(int64_t)15);
+    x.mb = (int)((M + x.n_tok - 1) / x.n_tok);
+    x.units = 0;
+    int kb_min = INT32_MAX, kb_max = 0;
+    for (int l = 0; l < g->n; ++l) {
+        const Plan& p = g->h[l]->plan;
+        x.units += (int64_t)p.S * x.mb;
+        kb_min = std::min(kb_min, p.KB);
+        kb_max = std::max(kb_max, p.KB);
+    }
+    x.P = q8_parts(x.units, kb_min, kb_max, (int)std::min<int64_t>(M, x.n_tok), q8_split_ctas(bn) * g->dev.sms, &x.us);
+    return x;
+}
+
+// The kernel an 8-bit call runs: the split-K kernel with 16- or 64-token units
+// (GEMV, M <= 64) or with 128-token units (GEMM_SINGLE, any M), or CTA pairs
+// with two strips per CTA (GEMM_WIDE, any M). AUTO and GEMM take GEMM_WIDE where
+// its estimate is the lower one: 8 us a call, 0.375 us a slab in every round of
+// quads and 4 us between two rounds. Measured, split-K and wide: 256 x 11008 x
+// 4096 16.5 and 19.8 us, 512 tokens 29.7 and 22.1, 768 (two rounds) 32.1 and 38.8,
+// 2048 79 and 54; 2048 x 4096 x 4096 32 and 36, 8192 x 512 x 2048 12.5 and 17.
+patch_status resolve_path_q8(patch_group g, int path, int64_t M, int* out) {
+    if (path == PATCH_PATH_AUTO && M <= kDecodeWideBN) path = PATCH_PATH_GEMV;
+    if (path == PATCH_PATH_AUTO || path == PATCH_PATH_GEMM) {
+        int64_t units = 0, slabs = 0;
+        for (int l = 0; l < g->n; ++l) {
+            const Plan& p = g->h[l]->plan;
+            const int64_t u = (p.S + 3) / 4 * ((M + kQ8WideBN - 1) / kQ8WideBN);
+            units += u;
+            slabs += u * p.KB;
+        }
+        const int64_t rounds = (units + g->dev.q8_wide_clusters - 1) / g->dev.q8_wide_clusters;
+        const double wide = 4.0 + rounds * (4.0 + 0.375 * slabs / std::max<int64_t>(1, units));
+        path = wide < q8_split_plan(g, kGemmBN, M).us ? PATCH_PATH_GEMM_WIDE : PATCH_PATH_GEMM_SINGLE;
+    }
+    if (path != PATCH_PATH_GEMV && path != PATCH_PATH_GEMM_SINGLE && path != PATCH_PATH_GEMM_WIDE)
+        return fail(PATCH_ERR_UNSUPPORTED, "path %d has no 8-bit kernel", path);
+    if (path == PATCH_PATH_GEMV && M > kDecodeWideBN)
+        return fail(PATCH_ERR_SHAPE, "the decode kernel takes M <= %d (got %lld)", kDecodeWideBN, (long long)M);
+    *out = path;
+    return PATCH_OK;
+}
+
+// The operands of an 8-bit call, one entry per member.
+struct Q8Call {
+    const int8_t* const* X;
+    const int64_t* ldx;           // NULL: contiguous
+    const float* const* x_scale;
+    int64_t M;
+    void* const* Y;
+    const int64_t* ldy;           // NULL: contiguous
+    int y_type;
+    // a single row needs no pitch, but its tensor map wants a multiple of 16 bytes
+    int64_t pitch_x(int l, int64_t K) const { return M == 1 ? (K + 15) & ~(int64_t)15 : ldx ? ldx[l] : K; }
+    int64_t pitch_y(int l, int64_t N) const { return ldy ? ldy[l] : N; }
+};
+
 template <int G>
 patch_status run_q8_split(patch_group g, const Q8Call& c, int path, cudaStream_t st) {
-    const int bn = path == PATCH_PATH_GEMM_SINGLE ? kGemmBN : c.M <= kDecodeBN ? kDecodeBN : kDecodeWideBN;
+    const Q8Split plan = q8_split_plan(
+        g, path == PATCH_PATH_GEMM_SINGLE ? kGemmBN : c.M <= kDecodeBN ? kDecodeBN : kDecodeWideBN, c.M);
+    if (plan.units > INT32_MAX / kQ8MaxParts)
+        return fail(PATCH_ERR_SHAPE, "M=%lld gives more than %d output tiles", (long long)c.M, INT32_MAX / kQ8MaxParts);
     Q8Maps<G> maps;
     Q8SplitArgs<G> a;
-    // token tiles of equal size, a multiple of 16
-    const int64_t mb = (c.M + bn - 1) / bn;
-    a.n_tok = (int)(((c.M + mb - 1) / mb + 15) & ~(int64_t)15);
-    a.MB = (int)((c.M + a.n_tok - 1) / a.n_tok);
+    a.n_tok = plan.n_tok;
+    a.MB = plan.mb;
+    a.P = plan.P;
     a.M = (int)c.M;
     a.n = g->n;
     a.status = g->status_dev;
-    int64_t units = 0;
-    int kb_min = INT32_MAX, kb_max = 0;
+    int units = 0;
     for (int l = 0; l < g->n; ++l) {
         patch_handle h = g->h[l];
         patch_status s = encode_codes(&maps.x[l], c.X[l], h->K, c.M, c.pitch_x(l, h->K), a.n_tok);
@@ -1036,16 +1072,10 @@ patch_status run_q8_split(patch_group g, const Q8Call& c, int path, cudaStream_t
         m.Y = c.Y[l];
         m.ldy = c.pitch_y(l, h->N);
         m.KB = h->plan.KB;
-        m.unit0 = (int)units;
-        units += (int64_t)h->plan.S * a.MB;
-        if (units > INT32_MAX / 8)
-            return fail(PATCH_ERR_SHAPE, "M=%lld gives more than %d output tiles", (long long)c.M, INT32_MAX / 8);
-        kb_min = std::min(kb_min, h->plan.KB);
-        kb_max = std::max(kb_max, h->plan.KB);
+        m.unit0 = units;
+        units += h->plan.S * a.MB;
     }
-    double us;
-    a.P = q8_parts(units, kb_min, kb_max, std::min(a.M, a.n_tok), q8_split_ctas(bn) * g->dev.sms, &us);
-    const cudaError_t e = launch_q8_split<G>(maps, a, bn, c.y_type, (int)units * a.P, st);
+    const cudaError_t e = launch_q8_split<G>(maps, a, plan.bn, c.y_type, units * a.P, st);
     if (e != cudaSuccess) return cuda_fail(e, "8-bit kernel launch");
     return PATCH_OK;
 }

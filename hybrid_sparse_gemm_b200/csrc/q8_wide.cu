@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 4; ++e) {
                         const uint32_t got = __shfl_xor_sync(0xffffffffu, p[k][e], 1);
                         const uint32_t two = __byte_perm(p[k][e], got, odd ? 0x3276 : 0x5410);
-                        if (8 * k + 2 * e < mrem) *reinterpret_cast<uint32_t*>(y + (8 * k + 2 * e) * ldy) = two;
+                        if (8 * k + 2 * e < mrem) __stcs(reinterpret_cast<uint32_t*>(y + (8 * k + 2 * e) * ldy), two);
                     }
                 }
             } else {
