@@ -81,8 +81,8 @@ patch_status check_flags(const uint8_t* flags, int64_t n) {
 struct DeviceInfo {
     int sms = 0;
     int pair_clusters = 0;  // co-resident 2-CTA clusters of the pair kernel
-    int q8_wide_clusters = 0;  // the same of its 8-bit counterpart
     int wide_clusters = 0;  // co-resident CTA pairs of the two-strips-per-CTA kernel
+    int q8_wide_clusters = 0;  // the same of its 8-bit counterpart (8-bit handles only)
 };
 std::mutex g_dev_mu;
 std::map<int, DeviceInfo> g_dev;
@@ -105,14 +105,27 @@ patch_status prepare_device(int* dev_out, DeviceInfo* info_out) {
         PATCH_CUDA(gemm_prepare_wide(&di.wide_clusters));
         if (di.wide_clusters <= 0) di.wide_clusters = 1;
         PATCH_CUDA(decode_prepare());
-        PATCH_CUDA(q8_prepare_split());
-        PATCH_CUDA(q8_prepare_wide(&di.q8_wide_clusters));
-        if (di.q8_wide_clusters <= 0) di.q8_wide_clusters = 1;
         if (di.pair_clusters <= 0) di.pair_clusters = 1;
         it = g_dev.emplace(dev, di).first;
     }
     *dev_out = dev;
     *info_out = it->second;
+    return PATCH_OK;
+}
+
+// The same for the 8-bit kernels, on a device's first 8-bit weight.
+std::map<int, int> g_dev_q8;  // device -> wide_clusters of the 8-bit kernel
+
+patch_status prepare_device_q8(int dev, DeviceInfo* info) {
+    std::lock_guard<std::mutex> lk(g_dev_mu);
+    auto it = g_dev_q8.find(dev);
+    if (it == g_dev_q8.end()) {
+        int clusters = 0;
+        PATCH_CUDA(q8_prepare_split());
+        PATCH_CUDA(q8_prepare_wide(&clusters));
+        it = g_dev_q8.emplace(dev, std::max(1, clusters)).first;
+    }
+    info->q8_wide_clusters = it->second;
     return PATCH_OK;
 }
 
@@ -597,7 +610,8 @@ patch_status make_group(const patch_handle* hs, int n, patch_group* out) {
         delete g;
         return fail(PATCH_ERR_CUDA, "group descriptor upload failed");
     }
-    patch_status st = alloc_ws(g, &g->capture_ws, nullptr);
+    // (the 8-bit kernels keep no workspace)
+    patch_status st = g->q8 ? PATCH_OK : alloc_ws(g, &g->capture_ws, nullptr);
     if (st == PATCH_OK && cudaDeviceSynchronize() != cudaSuccess) st = fail(PATCH_ERR_CUDA, "decode workspace set-up");
     if (st != PATCH_OK) {
         cudaFree(g->lins_dev);
@@ -1352,6 +1366,7 @@ patch_status pack_weights(const void* W_bf16, bool q8, const float* w_scale, int
     int dev = 0;
     DeviceInfo di;
     st = prepare_device(&dev, &di);
+    if (st == PATCH_OK && q8) st = prepare_device_q8(dev, &di);
     if (st != PATCH_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
 

@@ -755,7 +755,7 @@ cudaError_t launch_rows_type(const RowArgs& a, int mode, int sms, cudaStream_t s
 // values = code * scale, one product and one rounding per element, in groups
 // on the output's 16-byte boundaries. A thread takes kDeq groups, a block's row
 // apart: their loads are in flight together.
-constexpr int kDeq = 4;
+constexpr int kDeq = 2;
 template <class T>
 __global__ void __launch_bounds__(256) dequantize_kernel(const int8_t* q, int64_t ldq, const float* scale, int64_t M,
                                                          int K, int chunks, T* out, int64_t ldo) {
@@ -809,12 +809,13 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const int8_t* q, int64_
 template <class T>
 cudaError_t launch_deq(const int8_t* q, int64_t ldq, const float* scale, int64_t M, int K, T* out, int64_t ldo,
                        cudaStream_t st) {
-    // a block is 256 threads: as many to a row as give each kDeq groups, at least a warp
-    const int64_t groups = ((int64_t)K + 7) / 8 + 1;
-    unsigned x = 32;
-    while (x < 256 && x * kDeq < groups) x *= 2;
+    // a row in as few blocks as hold it at kDeq groups a thread, all but full (rows
+    // off the 16-byte boundaries may have a group more); short rows share a block
+    const bool aligned = K % 8 == 0 && ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(ldo * (int64_t)sizeof(T))) & 15u) == 0;
+    const int64_t groups = ((int64_t)K + 7) / 8 + (aligned ? 0 : 1);
+    const int chunks = (int)((groups + 256 * kDeq - 1) / (256 * kDeq));
+    const unsigned x = (unsigned)((groups + kDeq * chunks - 1) / (kDeq * chunks) + 31) / 32 * 32;
     const dim3 block(x, M < 256 / x ? (unsigned)M : 256 / x);
-    const int chunks = (int)((groups + x * kDeq - 1) / (x * kDeq));
     // whole rows per launch, within the grid's limit of 2^31 - 1 blocks
     const int64_t most = 2147483647ll / chunks * block.y;
     for (int64_t m0 = 0; m0 < M; m0 += most) {

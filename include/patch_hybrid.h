@@ -439,8 +439,14 @@ patch_status patch_selftest_wait(void* stream);
  * at least the row's length; ignored for one row). Unless a call says more,
  * pointers need the alignment of their elements only; rows of 16-byte multiples
  * on 16-byte boundaries are fastest. Outputs must not overlap inputs, except
- * where a call says so. M == 0 is a no-op. No call but patch_pack_q8
- * synchronises or, after the first call for an M, allocates.
+ * where a call says so. M == 0 is a no-op.
+ *
+ * Apart from patch_pack_q8, no call synchronises, allocates or keeps state: calls
+ * may overlap on the GPU (on one handle or group too), be captured in a CUDA graph
+ * from the first one on, and be replayed side by side. They are launched so that
+ * a kernel's set-up overlaps the end of the stream's previous kernel; memory is
+ * touched in stream order, but for the packed weights, which a product may read
+ * while the kernel before it still runs.
  */
 
 /*
@@ -455,7 +461,8 @@ patch_status patch_selftest_wait(void* stream);
  *            as for patch_pack; K <= 131008, so that the int32 sums of any
  *            codes are exact.
  * The handle works with patch_linear_q8, patch_unpack_q8, patch_info,
- * patch_copy_packed (whose tables then have KB = KC = ceil(K/128)), patch_check,
+ * patch_copy_packed (its slabs are 128 columns wide: KB = KC = ceil(K/128); a 2:4
+ * record is 8192 bytes of codes and its 2048-byte metadata block), patch_check,
  * patch_free, patch_group_create (with other 8-bit handles) and
  * patch_group_path; the bf16 calls refuse it (PATCH_ERR_ARG). A bf16 channel
  * that keeps a NaN or an infinity gives PATCH_ERR_ARG.
@@ -474,9 +481,12 @@ patch_status patch_pack_q8(const void* W, int w_type, const float* w_scale, int6
  *   Y        dev, M rows of N elements of y_type (PATCH_BF16, PATCH_FP16 or
  *            PATCH_FP32), 16-byte aligned, pitch ldy a multiple of 16 bytes.
  *            Every element of the N columns is written, nothing beside them.
- *   path     PATCH_PATH_AUTO, or a kernel of patch_path that has an 8-bit form
- *            (PATCH_ERR_UNSUPPORTED for the others): GEMM_SINGLE.
- * Schedules, workspaces, capture and concurrency as for patch_linear.
+ *   path     PATCH_PATH_AUTO, PATCH_PATH_GEMM, or a kernel of patch_path that has
+ *            an 8-bit form (PATCH_ERR_UNSUPPORTED for the others): GEMV (M <= 64;
+ *            units of 16 or 64 tokens, K split over a cluster), GEMM_SINGLE (the
+ *            same with units of 128 tokens) and GEMM_WIDE (CTA pairs, two strips
+ *            per CTA). AUTO takes GEMV up to 64 tokens, then the lower estimate.
+ * Every kernel gives the same bits.
  */
 patch_status patch_linear_q8(patch_handle h, const int8_t* X, int64_t ldx, const float* x_scale, int64_t M, void* Y,
                              int64_t ldy, int y_type, int path, void* stream);

@@ -159,6 +159,29 @@ def test_pitches_and_what_lies_beside(hsg, t, M):
         assert (frame[M:] == 7).all() and (frame[:, 384:] == 7).all()
 
 
+@pytest.mark.parametrize("M", [1, 16, 40, 100, 300])
+def test_long_rows(hsg, M):
+    """More slabs per row than a warp holds records of (32), and than the wide
+    kernel's tables hold (256)."""
+    K = 40000
+    w = Weight(hsg, 256, K, C=64, frac=0.5, seed=3)
+    x, sx = codes(gen("long", M), M, K).contiguous(), scales(gen("long", M), M)
+    want = w.product(x, sx)
+    for path in paths(hsg, M):
+        y = w.lin(x, sx, out_dtype=torch.float32, path=path)
+        w.lin.check()
+        assert_product(y, want)
+
+
+def test_kernels_agree_to_the_bit(hsg):
+    w = Weight(hsg, 640, 1152, frac=0.6, seed=12)
+    for M in (5, 64, 300):
+        x, sx = codes(gen("bits", M), M, 1152).contiguous(), scales(gen("bits", M), M)
+        for t in TYPES:
+            ys = [w.lin(x, sx, out_dtype=t, path=p) for p in paths(hsg, M)]
+            assert all(torch.equal(y, ys[0]) for y in ys)
+
+
 def test_largest_sums(hsg):
     """Every code -128 at the largest K: 128 * 128 * K = 2^31 - 2^20."""
     K = 131008
@@ -487,6 +510,72 @@ def test_capture_and_replay(hsg, M):
             again = torch.empty_like(q[i])
             hsg.patch_rmsnorm_q8(x[i], gamma, EPS, again, s[i])
             assert torch.equal(again, q[i])
+
+
+@pytest.mark.parametrize("M", [1, 30, 100, 600])
+def test_first_call_captured_and_graphs_side_by_side(hsg, M):
+    """No call needs a warm-up; two graphs of one group share nothing."""
+    ws = [Weight(hsg, 1024, 2048, frac=0.7, seed=s) for s in (21, 22)]
+    group = hsg.LinearGroupQ8([w.lin for w in ws])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    jobs = []
+    for i, st in enumerate(streams):
+        x, sx = codes(gen("side", M, i), M, 2048).contiguous(), scales(gen("side", M, i), M)
+        ys = [torch.empty(M, 1024, dtype=torch.float32, device="cuda") for _ in ws]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            for _ in range(5):
+                group(x, sx, outs=ys)
+        jobs.append((graph, x, sx, ys))
+    for _ in range(10):
+        for st, job in zip(streams, jobs):
+            with torch.cuda.stream(st):
+                job[0].replay()
+    torch.cuda.synchronize()
+    for _, x, sx, ys in jobs:
+        for w, y in zip(ws, ys):
+            assert_product(y, w.product(x, sx))
+
+
+@pytest.mark.parametrize("M", [1, 16, 50, 130, 500])
+def test_long_chain(hsg, M):
+    """Each kernel's set-up overlaps the one before it: a chain of dependent calls
+    on the same few buffers gives the bits that it gives one call at a time."""
+    hidden = 512
+    mix = Weight(hsg, hidden, hidden, frac=0.7, seed=31)
+    gate, up = Weight(hsg, hidden, hidden, frac=0.5, seed=32), Weight(hsg, hidden, hidden, frac=0.9, seed=33)
+    t = torch.bfloat16
+    gamma = torch.ones(hidden, dtype=t, device="cuda")
+    start = rows(gen("chain", M), M, hidden, t).contiguous()
+    group = hsg.LinearGroupQ8([gate.lin, up.lin])
+
+    def run(wait):
+        x, h = start.clone(), start.clone()
+        q, s = torch.empty(M, hidden, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+        ys = [torch.empty(M, hidden, dtype=t, device="cuda") for _ in range(2)]
+        for _ in range(25):
+            hsg.patch_rmsnorm_q8(x, gamma, EPS, q, s, residual=h, residual_out=h)
+            wait()
+            group(q, s, outs=ys)
+            wait()
+            hsg.patch_silu_mul_q8(ys[0], ys[1], q, s)
+            wait()
+            mix.lin(q, s, out=x)
+            wait()
+            hsg.patch_quantize_q8(x, q, s)
+            wait()
+            hsg.patch_dequantize_q8(q, s, x)
+            wait()
+            x.clamp_(-100, 100)
+        torch.cuda.synchronize()
+        return x, h
+
+    slow = run(torch.cuda.synchronize)
+    for _ in range(3):
+        fast = run(lambda: None)
+        assert torch.equal(fast[0], slow[0]) and torch.equal(fast[1], slow[1])
+    assert slow[0].isfinite().all() and slow[1].isfinite().all()
 
 
 @pytest.mark.parametrize("M", [1, 40, 100, 300])
