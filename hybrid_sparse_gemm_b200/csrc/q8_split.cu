@@ -111,13 +111,12 @@ __global__ void __launch_bounds__(kThreads, CTAS)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kSmemData);
     uint64_t* empty = full + STAGES;
     uint64_t* acc_full = empty + STAGES;
-    int* kind = reinterpret_cast<int*>(acc_full + 1);  // [STAGES] 1: the stage's slab is 2:4
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kind + STAGES);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     float* s_sw = reinterpret_cast<float*>(smem + C::kSmemData + 256);  // [kStrip] the rows' scales
     float* s_sx = s_sw + kStrip;                                        // [BN] the tokens' scales
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);  // known to be uniform
     const int lane = threadIdx.x & 31;
     const int P = a.P;
     const int rank = (int)blockIdx.x % P;
@@ -130,10 +129,10 @@ __global__ void __launch_bounds__(kThreads, CTAS)
     const int s = lu / a.MB, m0 = (lu % a.MB) * a.n_tok;
     const int b0 = (int)((int64_t)rank * L.KB / P), nb = (int)((int64_t)(rank + 1) * L.KB / P) - b0;
 
-    // the CTA's slab records, fetched while the barriers are set up
+    // the CTA's slab records, a lane each, fetched while the barriers are set up
     const uint32_t* drow = L.slab + (size_t)s * L.KB + b0;
     uint32_t d_now = 0, d_next = 0;
-    if (warp == 0) {
+    if (warp <= 1) {
         if (lane < nb) d_now = drow[lane];
         if (32 + lane < nb) d_next = drow[32 + lane];
     }
@@ -153,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, CTAS)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     auto raise = [&]() {
         *abort_flag = 1;
         atomicCAS(a.status, 0, kStatusTimeout);
@@ -171,7 +170,6 @@ __global__ void __launch_bounds__(kThreads, CTAS)
             const int st = i % STAGES;
             uint8_t* dst = smem + st * C::kStage;
             const bool sp = d & kSlabSparse;
-            kind[st] = sp;
             mbar_arrive_expect_tx(&full[st], q8_record_bytes(d) + (uint32_t)a.n_tok * 128u);
             const CUtensorMap* map = sp ? &maps.a10[l] : &maps.a16[l];
             const int at = (int)(slab_offset_bytes(d) >> 7);
@@ -221,26 +219,36 @@ __global__ void __launch_bounds__(kThreads, CTAS)
                 }
             }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ---------------- MMA issuer ----------------
-            const uint32_t idesc_d = idesc_i8(128, a.n_tok, false);
-            const uint32_t idesc_s = idesc_i8(128, a.n_tok, true);
-            const uint32_t e_col = tmem_base + BN;
-            for (int i = 0; i < nb; ++i) {
-                const int st = i % STAGES;
-                if (!mbar_wait(&full[st], (uint32_t)((i / STAGES) & 1), abort_flag)) {
-                    raise();
-                    break;
+        // ---------------- MMA issuer: the whole warp, one elected lane issuing ----------------
+        const uint32_t el = elect();
+        const uint32_t idesc_d = idesc_i8(128, a.n_tok, false);
+        const uint32_t idesc_s = idesc_i8(128, a.n_tok, true);
+        const uint32_t e_col = tmem_base + BN;
+        const uint32_t ring0 = smem_u32(smem);
+        uint32_t kinds = 0, st = 0, phase = 0;
+        for (int i = 0; i < nb; ++i) {
+            if (i % 32 == 0) {
+                if (i > 0) {
+                    d_now = d_next;
+                    if (i + 32 + lane < nb) d_next = drow[i + 32 + lane];
                 }
-                const uint32_t a_addr = smem_u32(smem + st * C::kStage);
-                const bool sp = kind[st];
-                if (sp) tc_cp_128x128b(e_col, smem_desc(a_addr + kSparseValBytes, 16, 128, kLayoutNone));
-                issue_slab_i8<false>(sp, i == 0, a_addr, a_addr + kStageA, tmem_base, e_col, idesc_d, idesc_s);
-                tc_commit(&empty[st]);
+                kinds = __ballot_sync(0xffffffffu, d_now & kSlabSparse);
             }
-            // after a timeout this still covers the MMAs that were issued
-            tc_commit(acc_full);
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[st], phase, abort_flag))) {
+                if (lane == 0) raise();
+                break;
+            }
+            const uint32_t a_addr = ring0 + st * (uint32_t)C::kStage;
+            issue_slab_i8<false>(el, (kinds >> (i % 32)) & 1u, i == 0, a_addr, a_addr + kStageA, tmem_base, e_col,
+                                 idesc_d, idesc_s);
+            commit_el(el, &empty[st]);
+            if (++st == STAGES) {
+                st = 0;
+                phase ^= 1u;
+            }
         }
+        // after a timeout this still covers the MMAs that were issued
+        commit_el(el, acc_full);
         __syncwarp();
         asm volatile("griddepcontrol.wait;" ::: "memory");
     } else {

@@ -13,7 +13,7 @@
 // measured to draw from L2. What feeds the pipe therefore decides the rate:
 // stages lie in a ring sized by their records (six 2:4 stages in flight), a
 // record and its metadata come in one copy, four warps issue copies and two
-// threads issue MMAs.
+// issue MMAs.
 //
 // TMEM: accumulators in columns [0, 224) and [256, 480), metadata of strip pair
 // 0 at 224 and of pair 1 at 232. All waits are bounded.
@@ -36,21 +36,19 @@ constexpr int kBN = kQ8WideBN;
 constexpr int kStageX = kBN / 2 * 128;          // 14 KB of activations per slab and CTA
 constexpr int kQ = 8;                           // per-stage barriers: more than the stages that fit in the ring
 constexpr int kMinStage = 2 * kQ8SparseBytes + kStageX;
-// Each producer warp keeps the slab records of its tile's two strips in shared
-// memory; weights with more slabs read them from global memory.
-constexpr int kTabKB = 256;                     // K up to 32768
-constexpr int kSmemTab = kProducers * 2 * kTabKB * 4;
 constexpr int kEpiCols = kBN / 2;               // columns of an epilogue warp
 constexpr int kSmemScales = kEpiWarps * kEpiCols * 4;
-constexpr int kRing = (232448 - kSmemTab - kSmemScales - 1024 - 512) / 1024 * 1024;
-constexpr int kSmemBytes = kRing + kSmemTab + kSmemScales + 1024 + 512;
+constexpr int kRing = (232448 - kSmemScales - 1024 - 512) / 1024 * 1024;
+constexpr int kSmemBytes = kRing + kSmemScales + 1024 + 512;
+constexpr uint32_t kDenseStage = 2 * kDenseSlabBytes + kStageX;
+constexpr uint32_t kSaved = kDenseSlabBytes - kQ8SparseBytes;  // by each 2:4 record of a stage
 static_assert(kStageX % 1024 == 0 && kQ8SparseBytes % 1024 == 0, "every record starts 1024-byte aligned");
 static_assert(kRing / kMinStage + 2 <= kQ, "stages in flight stay within the barrier window");
 // A wait for stage j's phase by parity is right only once stage j - kQ is known
-// to be consumed. A producer that loads stage g waits for a j <= g - 4 (a ring of
+// to be consumed. A producer that loads stage g waits for a j <= g - 3 (a ring of
 // at least four stages); its previous stage, g - kProducers, waited for one after
 // g - kProducers - kQ.
-static_assert(kProducers <= 4 && kRing / (2 * kDenseSlabBytes + kStageX) >= 4, "no wait is two phases ahead");
+static_assert(kProducers <= 4 && kRing / kDenseStage >= 4, "no wait is two phases ahead");
 // Registers: launched with 80 a thread (768 threads); the producers' warpgroup
 // gives up 24 of them and the issuers' 40, the four epilogue warpgroups take 16
 // more: 128 * (56 + 40 + 4 * 96) = 61440, what the block was launched with.
@@ -71,28 +69,49 @@ __device__ __forceinline__ int tile_tokens(const A& a, int j) {
     return 32 * (a.tile_gran + (j < a.tile_extra ? 1 : 0));
 }
 
-// What the MMA issuers need of a stage, written by the leader CTA's producer
-// that loads it, before the stage's loads are counted on its full barrier:
-// ring offset, record bytes of strip pair 0 | pair 1 << 16, and flags: bit 0
-// pair 0 is 2:4, bit 1 pair 1 is 2:4, bit 2 first stage of the tile, bit 3 last.
-struct StageDesc {
-    uint32_t off, bytes, flags;
-};
-
 // Stages are placed one after another in a ring of kRing bytes; a stage that
-// does not fit before the end starts again at 0. `pos` counts bytes placed so
-// far (including skipped ends); returns the ring offset of this stage.
+// does not fit before the end starts again at 0. Producers and issuers keep track
+// of all of them, in registers (with the ring's history in local memory the walk
+// took 470 cycles a stage, more than the stage's MMAs). `pos` counts bytes up to the
+// newest stage's end, skipped ends included (modulo 2^32: only differences are
+// used); the tail is the oldest stage whose bytes are not known to be free.
 struct Ring {
-    uint32_t pos = 0, off = 0;
-    __device__ __forceinline__ uint32_t place(uint32_t size) {
-        if (off + size > (uint32_t)kRing) {
+    uint32_t pos = 0, off = 0;            // end of the newest stage
+    uint32_t tail_pos = 0, tail_off = 0;  // start of stage `tail`
+    int tail = 0, next = 0;               // `next`: stages placed
+    uint64_t kinds = 0;                   // 4 bits a stage, newest lowest: 2:4 records | started at 0 again << 2
+    // Places a stage with `sparse` 2:4 records (0..2); returns its ring offset.
+    __device__ __forceinline__ uint32_t place(uint32_t sparse) {
+        const uint32_t size = kDenseStage - kSaved * sparse;
+        const bool wrap = off + size > (uint32_t)kRing;
+        if (wrap) {
             pos += (uint32_t)kRing - off;
             off = 0;
         }
+        kinds = (kinds << 4) | sparse | (wrap ? 4u : 0u);
         const uint32_t at = off;
         pos += size;
         off += size;
+        ++next;
         return at;
+    }
+    // Whether stages in the newest one's place have to be consumed first; then
+    // the tail moves past them, and the last of them is stage tail - 1.
+    __device__ __forceinline__ bool reclaim() {
+        bool any = false;
+        while ((int)(pos - (uint32_t)kRing - tail_pos) > 0) {
+            const int age = 4 * (next - 1 - tail);  // at most 4 * 11
+            const uint32_t size = kDenseStage - kSaved * ((uint32_t)(kinds >> age) & 3u);
+            tail_pos += size;
+            tail_off += size;
+            ++tail;
+            if ((uint32_t)(kinds >> (age - 4)) & 4u) {
+                tail_pos += (uint32_t)kRing - tail_off;
+                tail_off = 0;
+            }
+            any = true;
+        }
+        return any;
     }
 };
 
@@ -112,19 +131,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-    uint32_t* tabs = reinterpret_cast<uint32_t*>(smem + kRing);  // [warp][2][kTabKB]
-    float* scales = reinterpret_cast<float*>(smem + kRing + kSmemTab);  // [epilogue warp][kEpiCols]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kRing + kSmemTab + kSmemScales);
+    float* scales = reinterpret_cast<float*>(smem + kRing);  // [epilogue warp][kEpiCols]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kRing + kSmemScales);
     uint64_t* full = bars;                       // [kQ] leader: both CTAs' bytes of stage g (at g % kQ)
     uint64_t* empty = full + kQ;                 // [kQ] every CTA: stage g consumed by both issuers
     uint64_t* acc_full = empty + kQ;             // [2] both CTAs: accumulator h ready
     uint64_t* acc_empty = acc_full + 2;          // [2] leader: the 16 epilogue warps of accumulator h drained it
     uint64_t* drain = acc_empty + 2;             // [2]
-    StageDesc* sdesc = reinterpret_cast<StageDesc*>(drain + 2);  // [kQ] leader: stage g at g % kQ
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sdesc + kQ);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);  // known to be uniform
     const int lane = threadIdx.x & 31;
     const uint32_t pr = cluster_rank();          // CTA within the pair (0 = leader)
     const int cl = blockIdx.x >> 1;
@@ -150,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync();  // barriers of both CTAs initialised before any remote use
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     auto raise = [&]() {
         *abort_flag = 1;
         atomicCAS(a.status, 0, kStatusTimeout);
@@ -188,12 +205,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- producers (both CTAs) ----------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProduce));
         // Every producer walks the whole stage sequence to place each stage
-        // in the ring; it loads the stages g with g % kProducers == me.
-        // Before loading, the stages that last used those ring bytes must
-        // have been consumed (in order, so waiting for the latest suffices).
+        // in the ring; it loads the stages g with g % kProducers == me, whole
+        // warps together, lane 0 issuing. Before, the stages that last used those
+        // ring bytes must have been consumed (in order, so waiting for the latest
+        // suffices).
         const int me = warp;
         Ring ring;
-        uint32_t hist[kQ];   // ring positions where the last kQ stages started
         int g = 0;
         int my_last = -1;    // sequence index of the last stage this producer loaded
         bool ok = true;
@@ -206,8 +223,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // do not depend on the stream's previous kernel. Activations (at most two
         // of this warp's stages are then without theirs) follow once it is done.
         bool waited = false;
-        int n_pend = 0, pend_b[2], pend_l = 0, pend_tok = 0;
-        uint32_t pend_dst[2], pend_bar[2];
+        int n_pend = 0, pend_l = 0, pend_tok = 0, pend_b0 = 0, pend_b1 = 0;
+        uint32_t pend_dst0 = 0, pend_dst1 = 0, pend_bar0 = 0, pend_bar1 = 0;
+        auto load_pending = [&]() {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            waited = true;
+            if (lane == 0 && n_pend > 0)
+                tma_load_2d_pair_hint(pend_dst0, &maps.x[pend_l], pend_bar0, pend_b0 * kQ8SlabK, pend_tok, pol_x);
+            if (lane == 0 && n_pend > 1)
+                tma_load_2d_pair_hint(pend_dst1, &maps.x[pend_l], pend_bar1, pend_b1 * kQ8SlabK, pend_tok, pol_x);
+        };
         for (int u = cl; u < a.units && ok; u += pairs) {
             const Unit un = unit_of(u);
             const int l = un.l, c = un.c, j = un.j;
@@ -215,80 +240,64 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int KB = L.KB;
             const uint32_t* t0 = L.gemm + (size_t)pos_of(L.S, c, 0) * KB;
             const uint32_t* t1 = L.gemm + (size_t)pos_of(L.S, c, 1) * KB;
-            if (KB <= kTabKB) {
-                uint32_t* tab = tabs + warp * 2 * kTabKB;
-                for (int i = lane; i < KB; i += 32) {
-                    tab[i] = t0[i];
-                    tab[kTabKB + i] = t1[i];
-                }
-                t0 = tab;
-                t1 = tab + kTabKB;
-                __syncwarp();
-            }
             const int tok = tile_start(a, j) + (int)pr * (tile_tokens(a, j) >> 1);
-            for (int b = 0; lane == 0 && b < KB; ++b, ++g) {
-                const uint32_t d0 = t0[b], d1 = t1[b];
-                const uint32_t r0 = q8_record_bytes(d0), r1 = q8_record_bytes(d1);
-                const uint32_t size = r0 + r1 + (uint32_t)kStageX;
-                const uint32_t off = ring.place(size);
-                hist[g % kQ] = ring.pos - size;
-                if (g % kProducers != me) continue;
-                if (!waited && (ring.pos > (uint32_t)kRing || u != cl || n_pend == 2)) {
-                    asm volatile("griddepcontrol.wait;" ::: "memory");
-                    waited = true;
-                    for (int i = 0; i < n_pend; ++i)
-                        tma_load_2d_pair_hint(pend_dst[i], &maps.x[pend_l], pend_bar[i], pend_b[i] * kQ8SlabK, pend_tok,
-                                              pol_x);
+            // records of 32 slabs, a lane each, the next 32 on their way
+            uint32_t r0 = 0, r1 = 0, m0 = 0, m1 = 0;
+            uint32_t n0 = lane < KB ? t0[lane] : 0u, n1 = lane < KB ? t1[lane] : 0u;
+            for (int b = 0; b < KB; ++b, ++g) {
+                if ((b & 31) == 0) {
+                    r0 = n0;
+                    r1 = n1;
+                    m0 = __ballot_sync(0xffffffffu, r0 & kSlabSparse);
+                    m1 = __ballot_sync(0xffffffffu, r1 & kSlabSparse);
+                    const int nb = b + 32 + lane;
+                    n0 = nb < KB ? t0[nb] : 0u;
+                    n1 = nb < KB ? t1[nb] : 0u;
                 }
-                if (ring.pos > (uint32_t)kRing) {
-                    const uint32_t need = ring.pos - (uint32_t)kRing;
-                    int jl = -1;
-                    for (int jj = g - 1; jj >= 0 && jj > g - kQ; --jj)
-                        if (hist[jj % kQ] < need) {
-                            jl = jj;
-                            break;
-                        }
-                    if (jl >= 0 && !mbar_wait(&empty[jl % kQ], (uint32_t)((jl / kQ) & 1), abort_flag)) {
-                        raise();
+                const uint32_t s0 = (m0 >> (b & 31)) & 1u, s1 = (m1 >> (b & 31)) & 1u;
+                const uint32_t off = ring.place(s0 + s1);
+                if (g % kProducers != me) continue;
+                const bool reuse = ring.reclaim();
+                if (!waited && (reuse || u != cl || n_pend == 2)) load_pending();
+                if (reuse) {
+                    const int jl = ring.tail - 1;
+                    const bool free = mbar_wait(&empty[jl % kQ], (uint32_t)((jl / kQ) & 1), abort_flag);
+                    if (!__all_sync(0xffffffffu, free)) {
+                        if (lane == 0) raise();
                         ok = false;
                         break;
                     }
                 }
+                const uint32_t d0 = __shfl_sync(0xffffffffu, r0, b & 31), d1 = __shfl_sync(0xffffffffu, r1, b & 31);
+                const uint32_t b0 = q8_record_bytes(d0), b1 = q8_record_bytes(d1);
                 const uint32_t bar = map_to_rank(smem_u32(&full[g % kQ]), 0);
-                if (pr == 0) {
-                    StageDesc sd;
-                    sd.off = off;
-                    sd.bytes = r0 | (r1 << 16);
-                    sd.flags = (d0 & kSlabSparse) | ((d1 & kSlabSparse) << 1) | (b == 0 ? 4u : 0u) |
-                               (b + 1 == KB ? 8u : 0u);
-                    sdesc[g % kQ] = sd;
-                    mbar_arrive_expect_tx(&full[g % kQ], 2u * (r0 + r1 + x_bytes));
-                }
                 const uint32_t dst = smem_u32(smem) + off;
-                tma_load_2d_pair(dst, (d0 & kSlabSparse) ? &maps.a10[l] : &maps.a16[l], bar, 0,
-                                 (int)(slab_offset_bytes(d0) >> 7));
-                tma_load_2d_pair(dst + r0, (d1 & kSlabSparse) ? &maps.a10[l] : &maps.a16[l], bar, 0,
-                                 (int)(slab_offset_bytes(d1) >> 7));
-                if (waited) {
-                    tma_load_2d_pair_hint(dst + r0 + r1, &maps.x[l], bar, b * kQ8SlabK, tok, pol_x);
-                } else {
-                    pend_dst[n_pend] = dst + r0 + r1;
-                    pend_bar[n_pend] = bar;
-                    pend_b[n_pend++] = b;
+                if (lane == 0) {
+                    if (pr == 0) mbar_arrive_expect_tx(&full[g % kQ], 2u * (b0 + b1 + x_bytes));
+                    tma_load_2d_pair(dst, s0 ? &maps.a10[l] : &maps.a16[l], bar, 0, (int)(slab_offset_bytes(d0) >> 7));
+                    tma_load_2d_pair(dst + b0, s1 ? &maps.a10[l] : &maps.a16[l], bar, 0,
+                                     (int)(slab_offset_bytes(d1) >> 7));
+                    if (waited)
+                        tma_load_2d_pair_hint(dst + b0 + b1, &maps.x[l], bar, b * kQ8SlabK, tok, pol_x);
+                }
+                if (!waited) {
+                    if (n_pend == 0) {
+                        pend_dst0 = dst + b0 + b1;
+                        pend_bar0 = bar;
+                        pend_b0 = b;
+                    } else {
+                        pend_dst1 = dst + b0 + b1;
+                        pend_bar1 = bar;
+                        pend_b1 = b;
+                    }
+                    ++n_pend;
                     pend_l = l;
                     pend_tok = tok;
                 }
                 my_last = g;
             }
-            // the whole warp moves on to the next tile (or stops) with lane 0
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            __syncwarp();
         }
-        if (lane == 0 && !waited) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            for (int i = 0; i < n_pend; ++i)
-                tma_load_2d_pair_hint(pend_dst[i], &maps.x[pend_l], pend_bar[i], pend_b[i] * kQ8SlabK, pend_tok, pol_x);
-        }
+        if (!waited) load_pending();
         if (pr == 0 && lane == 0) {
             // Bounded wait for the loads of my stages among the last kQ of
             // the sequence, whatever the abort flag says, so none lands
@@ -303,46 +312,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < kEpiWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        if (lane == 0 && pr == 0 && warp < kMmaWarp + kMmaWarps) {
+        if (pr == 0 && warp < kMmaWarp + kMmaWarps) {
             // ---------------- MMA issuers (leader CTA), one per strip pair ----------------
-            // Both read every stage; a stage's ring bytes are free once both
-            // have committed it.
+            // Both read every stage; a stage's ring bytes are free once both have
+            // committed it. Whole warps, one elected lane issuing.
             const int h = warp - kMmaWarp;
+            const uint32_t el = elect();
             const uint32_t d_tmem = tmem_base + (uint32_t)(h * kAcc1);
             const uint32_t e_col = tmem_base + (uint32_t)(h ? kECol1 : kECol0);
             const uint32_t ring0 = smem_u32(smem);
+            Ring ring;
             int g = 0, t = 0;
             bool ok = true, any_mma = false;
             for (int u = cl; u < a.units && ok; u += pairs, ++t) {
-                const int nt = tile_tokens(a, unit_of(u).j);
+                const Unit un = unit_of(u);
+                const Q8WideMember& L = a.m[un.l];
+                const int KB = L.KB;
+                const uint32_t* t0 = L.gemm + (size_t)pos_of(L.S, un.c, 0) * KB;
+                const uint32_t* t1 = L.gemm + (size_t)pos_of(L.S, un.c, 1) * KB;
+                const int nt = tile_tokens(a, un.j);
                 const uint32_t idesc_d = idesc_i8(256, nt, false);
                 const uint32_t idesc_s = idesc_i8(256, nt, true);
-                if (!mbar_wait(&acc_empty[h], (t & 1) ^ 1u, abort_flag)) {
-                    raise();
+                uint32_t m0 = 0, m1 = 0;
+                uint32_t n0 = lane < KB ? t0[lane] : 0u, n1 = lane < KB ? t1[lane] : 0u;
+                if (!__all_sync(0xffffffffu, mbar_wait(&acc_empty[h], (t & 1) ^ 1u, abort_flag))) {
+                    if (lane == 0) raise();
                     break;
                 }
                 tc_fence_after();
-                for (bool last = false; !last; ++g) {
-                    if (!mbar_wait(&full[g % kQ], (uint32_t)((g / kQ) & 1), abort_flag)) {
-                        raise();
+                for (int b = 0; b < KB; ++b, ++g) {
+                    if ((b & 31) == 0) {
+                        m0 = __ballot_sync(0xffffffffu, n0 & kSlabSparse);
+                        m1 = __ballot_sync(0xffffffffu, n1 & kSlabSparse);
+                        const int nb = b + 32 + lane;
+                        n0 = nb < KB ? t0[nb] : 0u;
+                        n1 = nb < KB ? t1[nb] : 0u;
+                    }
+                    const uint32_t s0 = (m0 >> (b & 31)) & 1u, s1 = (m1 >> (b & 31)) & 1u;
+                    const uint32_t at = ring0 + ring.place(s0 + s1);
+                    const uint32_t b0 = kDenseSlabBytes - kSaved * s0, b1 = kDenseSlabBytes - kSaved * s1;
+                    if (!__all_sync(0xffffffffu,
+                                    mbar_wait(&full[g % kQ], (uint32_t)((g / kQ) & 1), abort_flag))) {
+                        if (lane == 0) raise();
                         ok = false;
                         break;
                     }
-                    const StageDesc sd = sdesc[g % kQ];
-                    const uint32_t r0 = sd.bytes & 0xFFFFu, r1 = sd.bytes >> 16;
-                    const bool sp = (sd.flags >> h) & 1u;
-                    last = (sd.flags & 8u) != 0;
-                    const uint32_t a_addr = ring0 + sd.off + (h ? r0 : 0u);
-                    if (sp) cp2_128x128b(e_col, smem_desc(a_addr + kSparseValBytes, 16, 128, kLayoutNone));
-                    issue_slab_i8<true>(sp, (sd.flags & 4u) != 0, a_addr, ring0 + sd.off + r0 + r1, d_tmem, e_col,
+                    issue_slab_i8<true>(el, h ? s1 : s0, b == 0, at + (h ? b0 : 0u), at + b0 + b1, d_tmem, e_col,
                                         idesc_d, idesc_s);
                     any_mma = true;
-                    commit2_mask(&empty[g % kQ], 3);
+                    commit2_mask_el(el, &empty[g % kQ], 3);
                 }
                 if (!ok) break;
-                commit2_mask(&acc_full[h], 3);
+                commit2_mask_el(el, &acc_full[h], 3);
             }
-            if (*abort_flag && any_mma) {
+            __syncwarp();
+            if (*abort_flag && any_mma && el) {
                 commit2_local(&drain[h]);
                 const uint64_t t0 = globaltimer();
                 while (!mbar_try_wait(&drain[h], 0) && globaltimer() - t0 < kWaitLimitNs) {
