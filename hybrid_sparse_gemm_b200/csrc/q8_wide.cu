@@ -125,6 +125,24 @@ __device__ __forceinline__ uint32_t pack2(float x, float y, __half) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Two products at once, each rounded as a * b is.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+template <class T>
+__device__ __forceinline__ uint32_t pack2(uint64_t v, T t) {
+    float x, y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+    return pack2(x, y, t);
+}
+
 template <int G, class T>
 __global__ void __launch_bounds__(kThreads, 1)
     q8_wide_kernel(const __grid_constant__ Q8Maps<G> maps, const __grid_constant__ Q8WideArgs<G> a) {
@@ -335,11 +353,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t idesc_s = idesc_i8(256, nt, true);
                 uint32_t m0 = 0, m1 = 0;
                 uint32_t n0 = lane < KB ? t0[lane] : 0u, n1 = lane < KB ? t1[lane] : 0u;
-                if (!__all_sync(0xffffffffu, mbar_wait(&acc_empty[h], (t & 1) ^ 1u, abort_flag))) {
-                    if (lane == 0) raise();
-                    break;
-                }
-                tc_fence_after();
                 for (int b = 0; b < KB; ++b, ++g) {
                     if ((b & 31) == 0) {
                         m0 = __ballot_sync(0xffffffffu, n0 & kSlabSparse);
@@ -351,12 +364,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t s0 = (m0 >> (b & 31)) & 1u, s1 = (m1 >> (b & 31)) & 1u;
                     const uint32_t at = ring0 + ring.place(s0 + s1);
                     const uint32_t b0 = kDenseSlabBytes - kSaved * s0, b1 = kDenseSlabBytes - kSaved * s1;
-                    if (!__all_sync(0xffffffffu,
-                                    mbar_wait(&full[g % kQ], (uint32_t)((g / kQ) & 1), abort_flag))) {
+                    ok = mbar_wait(&full[g % kQ], (uint32_t)((g / kQ) & 1), abort_flag);
+                    // the first stage of a tile is at hand before the accumulator is
+                    if (b == 0) ok = ok && mbar_wait(&acc_empty[h], (t & 1) ^ 1u, abort_flag);
+                    if (!__all_sync(0xffffffffu, ok)) {
                         if (lane == 0) raise();
                         ok = false;
                         break;
                     }
+                    if (b == 0) tc_fence_after();
                     issue_slab_i8<true>(el, h ? s1 : s0, b == 0, at + (h ? b0 : 0u), at + b0 + b1, d_tmem, e_col,
                                         idesc_d, idesc_s);
                     any_mma = true;
@@ -413,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // first store: all CTAs finish a tile at about the same time,
                 // and the burst of stores then overlaps the next tile's MMAs.
                 // Eight columns at a time, the next eight on their way.
+                const uint64_t sw2 = pair2(sw, sw);
                 uint32_t p[kEpiCols / 8][4], buf[2][8];
                 tmem_ld_32x32b_x8(taddr, buf[0]);
                 tc_wait_ld();
@@ -423,10 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (8 * (k + 1) < cols) tmem_ld_32x32b_x8(taddr + 8 * (k + 1), buf[(k + 1) & 1]);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float4 f = *reinterpret_cast<const float4*>(sx + 8 * k + 4 * e);
-                        p[k][2 * e] = pack2((float)(int)v[4 * e] * f.x * sw, (float)(int)v[4 * e + 1] * f.y * sw, T());
-                        p[k][2 * e + 1] =
-                            pack2((float)(int)v[4 * e + 2] * f.z * sw, (float)(int)v[4 * e + 3] * f.w * sw, T());
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(sx + 8 * k + 4 * e);
+                        const uint32_t* u = v + 4 * e;
+                        p[k][2 * e] = pack2(mul2(mul2(pair2((float)(int)u[0], (float)(int)u[1]), f.x), sw2), T());
+                        p[k][2 * e + 1] = pack2(mul2(mul2(pair2((float)(int)u[2], (float)(int)u[3]), f.y), sw2), T());
                     }
                     tc_wait_ld();
                 }
