@@ -967,39 +967,25 @@ patch_status run_group(patch_group g, const void* const* X, int64_t M, void* con
     return PATCH_OK;
 }
 
-// Parts of K of the split-K kernel, at least a slab each: the least of an
-// estimate in us, fitted to calls of 512 to 11008 rows, 2048 to 11008 columns and
-// 1 to 100 tokens with every P (within 8 % of the best P in all of them). Slabs
-// follow one another at 0.25 us in a CTA, a wave of CTAs costs 1 us more (95 % of
-// the slots fill: a cluster stays within a GPC), and every CTA takes 5 ns, and
-// 0.16 ns a token for its sums, of the whole GPU.
-int q8_parts(int64_t units, int kb_min, int kb_max, int tokens, int slots, double* us) {
-    double best = 1e300;
-    int parts = 1;
-    for (int p = 1; p <= std::min(kQ8MaxParts, kb_min); ++p) {
-        const int64_t at_once = std::max(1, (int)(0.95 * slots / p));
-        const double waves = (double)((units + at_once - 1) / at_once);
-        const double cost =
-            waves * (0.25 * ((kb_max + p - 1) / p) + 1.0) + (double)(units * p) * (0.005 + 0.00016 * tokens);
-        if (cost < best) {
-            best = cost;
-            parts = p;
-        }
-    }
-    *us = best;
-    return parts;
-}
-
-// How the split-K kernel cuts a call: bn tokens per unit at most, mb tiles of
-// n_tok tokens (equal ones, a multiple of 16), P parts of K.
+// How the split-K kernel cuts a call: its form, mb tiles of n_tok tokens (equal
+// ones, a multiple of 16), P parts of K.
 struct Q8Split {
-    int bn, mb, n_tok, P;
+    int config, mb, n_tok, P;
     int64_t units;
     double us;  // estimate
 };
+
+// The form with units of bn tokens and the parts of K, at least a slab each, of the
+// least estimate in us. It was fitted to every form and every P for calls of 512 to
+// 13824 rows, 2048 to 11008 columns and 1 to 512 tokens: the choice is within 1 % of
+// the best on average, 13 % at worst, and the estimate of calls of 65 tokens or more
+// within 17 %. A call takes 2 us. Slabs follow one another in a CTA at 0.14 us with
+// six stages or more, at 0.216 with fewer (two CTAs then share an SM's bandwidth); a
+// wave of CTAs costs 1.5 and 2.1 us more (95 % of the slots fill where clusters have
+// to stay within a GPC), and every CTA takes 10 ns, and 0.12 ns a token for its sums,
+// of the whole GPU.
 Q8Split q8_split_plan(patch_group g, int bn, int64_t M) {
     Q8Split x;
-    x.bn = bn;
     const int64_t mb = (M + bn - 1) / bn;
     x.n_tok = (int)(((M + mb - 1) / mb + 15) & ~(int64_t)15);
     x.mb = (int)((M + x.n_tok - 1) / x.n_tok);
@@ -1011,7 +997,27 @@ Q8Split q8_split_plan(patch_group g, int bn, int64_t M) {
         kb_min = std::min(kb_min, p.KB);
         kb_max = std::max(kb_max, p.KB);
     }
-    x.P = q8_parts(x.units, kb_min, kb_max, (int)std::min<int64_t>(M, x.n_tok), q8_split_ctas(bn) * g->dev.sms, &x.us);
+    const double tokens = (double)std::min<int64_t>(M, x.n_tok);
+    x.us = 1e300;
+    x.config = 0;
+    x.P = 1;
+    int config = 0;
+    for (const Q8SplitConfig& c : kQ8SplitConfigs) {
+        const bool deep = c.stages >= 6;
+        for (int p = 1; c.bn == bn && p <= std::min(kQ8MaxParts, kb_min); ++p) {
+            const int slots = c.ctas * g->dev.sms;
+            const int64_t at_once = p == 1 ? slots : std::max(1, (int)(0.95 * slots / p));
+            const double waves = (double)((x.units + at_once - 1) / at_once);
+            const double us = 2.0 + waves * ((deep ? 0.14 : 0.216) * ((kb_max + p - 1) / p) + (deep ? 1.5 : 2.1)) +
+                              (double)(x.units * p) * (0.01 + 0.00012 * tokens);
+            if (us < x.us) {
+                x.us = us;
+                x.config = config;
+                x.P = p;
+            }
+        }
+        ++config;
+    }
     return x;
 }
 
@@ -1033,7 +1039,7 @@ patch_status resolve_path_q8(patch_group g, int path, int64_t M, int* out) {
             slabs += u * p.KB;
         }
         const int64_t rounds = (units + g->dev.q8_wide_clusters - 1) / g->dev.q8_wide_clusters;
-        const double wide = 4.0 + rounds * (4.0 + 0.375 * slabs / std::max<int64_t>(1, units));
+        const double wide = 4.0 + rounds * (4.0 + 0.34 * slabs / std::max<int64_t>(1, units));
         path = wide < q8_split_plan(g, kGemmBN, M).us ? PATCH_PATH_GEMM_WIDE : PATCH_PATH_GEMM_SINGLE;
     }
     if (path != PATCH_PATH_GEMV && path != PATCH_PATH_GEMM_SINGLE && path != PATCH_PATH_GEMM_WIDE)
@@ -1089,7 +1095,7 @@ patch_status run_q8_split(patch_group g, const Q8Call& c, int path, cudaStream_t
         m.unit0 = units;
         units += h->plan.S * a.MB;
     }
-    const cudaError_t e = launch_q8_split<G>(maps, a, plan.bn, c.y_type, units * a.P, st);
+    const cudaError_t e = launch_q8_split<G>(maps, a, plan.config, c.y_type, units * a.P, st);
     if (e != cudaSuccess) return cuda_fail(e, "8-bit kernel launch");
     return PATCH_OK;
 }

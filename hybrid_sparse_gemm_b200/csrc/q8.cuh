@@ -70,12 +70,24 @@ struct Q8SplitArgs {
     int n_tok;  // tokens per tile, a multiple of 16
     int P;      // CTAs per unit
 };
-// grid: all units * P; bn: 16, 64 or 128 (n_tok at most)
+// The kernel's forms: tokens per unit (n_tok at most), pipeline stages, CTAs
+// resident per SM. They share the SM's shared memory. One CTA with a deep pipeline
+// streams its slabs faster than two shallow ones side by side and joins fewer sums,
+// as long as one CTA per SM is the whole call; with more CTAs than that, one joins
+// and stores while the other streams. Measured at 2:4 tiles 70 %, the better P of
+// each, one deep and two shallow: 100 x 4096 x 4096 6.6 and 8.3 us, 100 x 11008 x
+// 4096 10.4 and 11.6, 64 x 4096 x 4096 6.2 and 6.7, 200 x 11008 x 4096 (172 units)
+// 18.1 and 14.9. 16 tokens: 6 stages x 2 CTAs 4.6 us at 4096 x 4096, 4 x 3 4.8, 3 x
+// 4 5.0, 12 x 1 5.1; 4096 x 11008 8.8, 9.2, 9.6 and 9.1.
+struct Q8SplitConfig {
+    int bn, stages, ctas;
+};
+constexpr Q8SplitConfig kQ8SplitConfigs[] = {{16, 6, 2}, {64, 9, 1}, {64, 4, 2}, {128, 6, 1}, {128, 3, 2}};
+// grid: all units * P; config: index into kQ8SplitConfigs
 template <int G>
-cudaError_t launch_q8_split(const Q8Maps<G>& maps, const Q8SplitArgs<G>& a, int bn, int y_type, int grid,
+cudaError_t launch_q8_split(const Q8Maps<G>& maps, const Q8SplitArgs<G>& a, int config, int y_type, int grid,
                             cudaStream_t st);
 constexpr int kQ8MaxParts = 8;
-int q8_split_ctas(int bn);  // CTAs resident per SM
 cudaError_t q8_prepare_split();
 
 // Kernel on CTA pairs with two strips per CTA (many tokens). A work unit is

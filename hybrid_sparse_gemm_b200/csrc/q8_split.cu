@@ -346,11 +346,9 @@ cudaError_t launch(const Q8Maps<G>& maps, const Q8SplitArgs<G>& a, int grid, cud
     return cudaLaunchKernelEx(&cfg, q8_split_kernel<BN, STAGES, CTAS, G, T>, maps, a);
 }
 
-// BN tokens per unit; stages and resident CTAs share the SM's shared memory. More
-// CTAs keep more slabs in flight, but each joins and stores sums. Measured at 4096
-// x 4096 (2:4 tiles 70 %): one token 4.7 us with 3 stages x 4 CTAs, 5.4 with 6 x 2;
-// 64 tokens 6.7 us with 4 x 2, 7.3 with 3 x 3.
-#define Q8_SPLIT_CONFIGS(X) X(16, 3, 4) X(64, 4, 2) X(128, 3, 2)
+#define Q8_SPLIT_CONFIGS(X) X(0) X(1) X(2) X(3) X(4)
+static_assert(sizeof(kQ8SplitConfigs) / sizeof(kQ8SplitConfigs[0]) == 5, "every form is listed");
+#define Q8_PARAMS(I) kQ8SplitConfigs[I].bn, kQ8SplitConfigs[I].stages, kQ8SplitConfigs[I].ctas
 
 template <int BN, int STAGES, int CTAS>
 cudaError_t prepare_all() {
@@ -366,31 +364,23 @@ cudaError_t prepare_all() {
 
 }  // namespace
 
-int q8_split_ctas(int bn) {
-#define Q8_CTAS(BN, STAGES, CTAS) \
-    if (bn == BN) return CTAS;
-    Q8_SPLIT_CONFIGS(Q8_CTAS)
-#undef Q8_CTAS
-    return 1;
-}
-
 cudaError_t q8_prepare_split() {
     cudaError_t e = cudaSuccess;
-#define Q8_PREPARE(BN, STAGES, CTAS) \
-    if (e == cudaSuccess) e = prepare_all<BN, STAGES, CTAS>();
+#define Q8_PREPARE(I) \
+    if (e == cudaSuccess) e = prepare_all<Q8_PARAMS(I)>();
     Q8_SPLIT_CONFIGS(Q8_PREPARE)
 #undef Q8_PREPARE
     return e;
 }
 
 template <int G>
-cudaError_t launch_q8_split(const Q8Maps<G>& maps, const Q8SplitArgs<G>& a, int bn, int y_type, int grid,
+cudaError_t launch_q8_split(const Q8Maps<G>& maps, const Q8SplitArgs<G>& a, int config, int y_type, int grid,
                             cudaStream_t st) {
-#define Q8_LAUNCH(BN, STAGES, CTAS)                                                                 \
-    if (bn == BN)                                                                                   \
-        return y_type == kBf16   ? launch<BN, STAGES, CTAS, G, __nv_bfloat16>(maps, a, grid, st)    \
-               : y_type == kFp16 ? launch<BN, STAGES, CTAS, G, __half>(maps, a, grid, st)           \
-                                 : launch<BN, STAGES, CTAS, G, float>(maps, a, grid, st);
+#define Q8_LAUNCH(I)                                                                        \
+    if (config == I)                                                                        \
+        return y_type == kBf16   ? launch<Q8_PARAMS(I), G, __nv_bfloat16>(maps, a, grid, st) \
+               : y_type == kFp16 ? launch<Q8_PARAMS(I), G, __half>(maps, a, grid, st)        \
+                                 : launch<Q8_PARAMS(I), G, float>(maps, a, grid, st);
     Q8_SPLIT_CONFIGS(Q8_LAUNCH)
 #undef Q8_LAUNCH
     return cudaErrorInvalidValue;
