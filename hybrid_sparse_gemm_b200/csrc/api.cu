@@ -1024,10 +1024,11 @@ Q8Split q8_split_plan(patch_group g, int bn, int64_t M) {
 // The kernel an 8-bit call runs: the split-K kernel with 16- or 64-token units
 // (GEMV, M <= 64) or with 128-token units (GEMM_SINGLE, any M), or CTA pairs
 // with two strips per CTA (GEMM_WIDE, any M). AUTO and GEMM take GEMM_WIDE where
-// its estimate is the lower one: 8 us a call, 0.375 us a slab in every round of
+// its estimate is the lower one: 8 us a call, 0.34 us a slab in every round of
 // quads and 4 us between two rounds. Measured, split-K and wide: 256 x 11008 x
-// 4096 16.5 and 19.8 us, 512 tokens 29.7 and 22.1, 768 (two rounds) 32.1 and 38.8,
-// 2048 79 and 54; 2048 x 4096 x 4096 32 and 36, 8192 x 512 x 2048 12.5 and 17.
+// 4096 15.4 and 17.7 us, 512 tokens 28.1 and 20.4, 768 (two rounds) 30.5 and 32.8,
+// 2048 76 and 48; 2048 x 4096 x 4096 29.7 and 33.1, 300 x 13824 x 5120 30.7 and 20.5,
+// 2048 x 512 x 2048 5.7 and 13.4.
 patch_status resolve_path_q8(patch_group g, int path, int64_t M, int* out) {
     if (path == PATCH_PATH_AUTO && M <= kDecodeWideBN) path = PATCH_PATH_GEMV;
     if (path == PATCH_PATH_AUTO || path == PATCH_PATH_GEMM) {

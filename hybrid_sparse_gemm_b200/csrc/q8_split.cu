@@ -161,10 +161,10 @@ __global__ void __launch_bounds__(kThreads, CTAS)
 
     if (warp == 0) {
         // ---------------- producer ----------------
-        // Weights first out of L2, which leaves the activations in it: 100 x 11008 x
-        // 4096 12.2 us, without the hint 12.9. With 16 tokens there is nothing to
-        // spare, and weights that fit may stay: 1 x 11008 x 4096 7.2 us, with it 7.7.
-        constexpr bool kHint = BN > kDecodeBN;
+        // Weights first out of L2, which leaves the activations in it, and what the
+        // neighbours of this call left. Five layers' weights in turn, with the hint and
+        // without: 100 x 11008 x 4096 10.1 and 11.0 us, 16 tokens 8.3 and 8.8; where the
+        // five fit in L2 (4096 x 4096) it costs 3 %, but a model's weights do not.
         const uint64_t pol_w = policy_evict_first();
         auto load_w = [&](int i, uint32_t d) {
             const int st = i % STAGES;
@@ -173,10 +173,7 @@ __global__ void __launch_bounds__(kThreads, CTAS)
             mbar_arrive_expect_tx(&full[st], q8_record_bytes(d) + (uint32_t)a.n_tok * 128u);
             const CUtensorMap* map = sp ? &maps.a10[l] : &maps.a16[l];
             const int at = (int)(slab_offset_bytes(d) >> 7);
-            if (kHint)
-                tma_load_2d_hint(dst, map, &full[st], 0, at, pol_w);
-            else
-                tma_load_2d(dst, map, &full[st], 0, at);
+            tma_load_2d_hint(dst, map, &full[st], 0, at, pol_w);
         };
         auto load_x = [&](int i) {
             const int st = i % STAGES;
