@@ -9,11 +9,17 @@
 // tokens. Every 128-column slab issues two 256-row MMAs (cta_group::2), one per
 // strip pair, so that each activation byte from L2 serves 512 weight rows: per
 // slab and CTA 20 KB of 2:4 records and 14 KB of activations feed 448 cycles of
-// the tensor pipe, 76 bytes a cycle, a little above the 68 that one SM was
-// measured to draw from L2. What feeds the pipe therefore decides the rate:
-// stages lie in a ring sized by their records (six 2:4 stages in flight), a
-// record and its metadata come in one copy, four warps issue copies and two
-// issue MMAs.
+// the tensor pipe, 76 bytes a cycle. Stages lie in a ring sized by their records
+// (six 2:4 stages in flight), a record and its metadata come in one copy, four
+// warps issue copies and two issue MMAs, whole warps with an elected lane.
+//
+// Measured: one CTA pair alone takes 457 cycles a 2:4 stage and 905 a dense one, the
+// pipe's own pace; all pairs together 1.0 to 1.15 times that. Between two tiles of a
+// pair the accumulators are read for 3300 cycles, a sixth of a tile of 32 slabs,
+// but taking the conversions out of it won 1 % of the time only: 2048 x 11008 x
+// 4096 with 90 % 2:4 tiles takes 48 us at the clock of a short run (its MMAs 31 us at
+// twice the bf16 matrix rate), 8192 x 13824 x 5120 253 us, and in a run of seconds,
+// where the card's power limit holds the clock near 1.4 GHz, 301 us.
 //
 // TMEM: accumulators in columns [0, 224) and [256, 480), metadata of strip pair
 // 0 at 224 and of pair 1 at 232. All waits are bounded.
@@ -71,8 +77,8 @@ __device__ __forceinline__ int tile_tokens(const A& a, int j) {
 
 // Stages are placed one after another in a ring of kRing bytes; a stage that
 // does not fit before the end starts again at 0. Producers and issuers keep track
-// of all of them, in registers (with the ring's history in local memory the walk
-// took 470 cycles a stage, more than the stage's MMAs). `pos` counts bytes up to the
+// of all of them, in registers (with the ring's history in local memory a step of
+// the walk took 470 cycles, more than the stage's MMAs). `pos` counts bytes up to the
 // newest stage's end, skipped ends included (modulo 2^32: only differences are
 // used); the tail is the oldest stage whose bytes are not known to be free.
 struct Ring {
