@@ -352,11 +352,21 @@ def patch_dequantize_q8(q: torch.Tensor, scale: torch.Tensor, out: torch.Tensor,
     _check(_binding.dequantize_q8(q, scale, out, stream))
 
 
-def _codes_like(x: torch.Tensor):
+def _empty(shape, dtype, device, stream):
+    """Memory for a call on `stream`: from that stream's pool, so that no earlier or
+    later owner of the same memory on another stream overlaps the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    raw = _stream(stream)
+    with torch.cuda.stream(torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _codes_like(x: torch.Tensor, stream):
     """Fresh (codes, scales) for the rows of x; the codes' pitch suits the products."""
     M, K = x.shape
-    q = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=x.device)[:, :K]
-    return q, torch.empty(M, dtype=torch.float32, device=x.device)
+    q = _empty((M, (K + 15) // 16 * 16), torch.int8, x.device, stream)[:, :K]
+    return q, _empty(M, torch.float32, x.device, stream)
 
 
 class LinearGroup:
@@ -493,17 +503,17 @@ class PackedLinearQ8:
         if x_scale is None:
             x = X
             out_dtype = out_dtype or X.dtype
-            X, x_scale = _codes_like(x)
+            X, x_scale = _codes_like(x, stream)
             patch_quantize_q8(x, X, x_scale, stream)
         if out is None:
-            out = torch.empty((X.shape[0], self.N), dtype=out_dtype or torch.bfloat16, device=X.device)
+            out = _empty((X.shape[0], self.N), out_dtype or torch.bfloat16, X.device, stream)
         _check(_binding.linear_q8(self.handle, self.N, self.K, X, x_scale, out, path, stream))
         return out
 
     def unpack(self, stream=None):
         """(masked codes int8 [N,K], channel scales fp32 [N])."""
-        W = torch.empty((self.N, self.K), dtype=torch.int8, device="cuda")
-        w_scale = torch.empty(self.N, dtype=torch.float32, device="cuda")
+        W = _empty((self.N, self.K), torch.int8, "cuda", stream)
+        w_scale = _empty(self.N, torch.float32, "cuda", stream)
         patch_unpack_q8(self.handle, W, w_scale, stream)
         return W, w_scale
 
@@ -548,7 +558,7 @@ class LinearGroupQ8:
             raise ValueError(f"the group has {n} members")
         M = Xs[0].shape[0]
         if outs is None:
-            outs = [torch.empty((M, l.N), dtype=out_dtype, device=Xs[0].device) for l in self.linears]
+            outs = [_empty((M, l.N), out_dtype, Xs[0].device, stream) for l in self.linears]
         ldx, ldy = (_I64 * n)(), (_I64 * n)()
         for i, l in enumerate(self.linears):
             ldx[i] = _rows(f"X {i}", Xs[i], (M, l.K), torch.int8)
@@ -563,7 +573,7 @@ class LinearGroupQ8:
 
     def quantize(self, x, outs=None, path: int = PATH_AUTO, stream=None):
         """The products of the rows of x, quantised once for all members."""
-        q, scale = _codes_like(x)
+        q, scale = _codes_like(x, stream)
         patch_quantize_q8(x, q, scale, stream)
         return self(q, scale, outs, x.dtype, path, stream)
 
@@ -571,14 +581,14 @@ class LinearGroupQ8:
         """(products of the RMS norm of x + residual, x + residual); without a
         residual, (products of the norm of x, x)."""
         if residual is not None and residual_out is None:
-            residual_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        q, scale = _codes_like(x)
+            residual_out = _empty(x.shape, x.dtype, x.device, stream)
+        q, scale = _codes_like(x, stream)
         patch_rmsnorm_q8(x, gamma, eps, q, scale, residual, residual_out, stream)
         return self(q, scale, outs, x.dtype, path, stream), x if residual is None else residual_out
 
     def silu_mul(self, gate, up, outs=None, path: int = PATH_AUTO, stream=None):
         """The products of silu(gate) * up."""
-        q, scale = _codes_like(gate)
+        q, scale = _codes_like(gate, stream)
         patch_silu_mul_q8(gate, up, q, scale, stream)
         return self(q, scale, outs, gate.dtype, path, stream)
 

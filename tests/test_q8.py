@@ -604,6 +604,40 @@ def test_streams_and_threads(hsg, M):
         assert_product(a, b)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_memory_of_a_call_belongs_to_its_stream(hsg, raw, monkeypatch):
+    """What a call on a named stream allocates is not handed to the current
+    stream while the call may still run."""
+    M, N, K = 40, 512, 1024
+    w = Weight(hsg, N, K, frac=0.7, seed=9)
+    group = hsg.LinearGroupQ8([w.lin])
+    x = rows(gen("own"), M, K, torch.bfloat16).contiguous()
+    gamma = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    used = []
+    for name in ("patch_quantize_q8", "patch_rmsnorm_q8", "patch_silu_mul_q8"):
+        def record(*args, f=getattr(hsg, name), **kw):
+            used.extend((t.untyped_storage().data_ptr(), t.untyped_storage().nbytes()) for t in args
+                        if isinstance(t, torch.Tensor) and t is not x and t is not gamma)
+            return f(*args, **kw)
+        monkeypatch.setattr(hsg, name, record)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    for call in (lambda st: w.lin(x, stream=st), lambda st: group.quantize(x, stream=st)[0],
+                 lambda st: group.norm(x, gamma, 1e-5, x, stream=st)[0][0],
+                 lambda st: group.silu_mul(x, x, stream=st)[0]):
+        used.clear()
+        y = call(stream.cuda_stream if raw else stream)
+        used.append((y.untyped_storage().data_ptr(), y.untyped_storage().nbytes()))
+        assert len(used) >= 3
+        del y
+        fresh = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in used for _ in range(3)]
+        assert not {t.data_ptr() for t in fresh} & {p for p, _ in used}
+        torch.cuda.synchronize()
+        assert torch.equal(call(stream), call(None).clone())
+        torch.cuda.synchronize()
+        del fresh
+
+
 def test_handles_come_and_go(hsg):
     before = None
     for i in range(6):
