@@ -1030,6 +1030,8 @@ Q8Split q8_split_plan(patch_group g, int bn, int64_t M) {
 // 2048 76 and 48; 2048 x 4096 x 4096 29.7 and 33.1, 300 x 13824 x 5120 30.7 and 20.5,
 // 2048 x 512 x 2048 5.7 and 13.4.
 patch_status resolve_path_q8(patch_group g, int path, int64_t M, int* out) {
+    if (M > (int64_t)INT32_MAX / 2) return fail(PATCH_ERR_SHAPE, "M too large");
+    M = std::max<int64_t>(1, M);  // patch_group_path may ask about a call that does nothing
     if (path == PATCH_PATH_AUTO && M <= kDecodeWideBN) path = PATCH_PATH_GEMV;
     if (path == PATCH_PATH_AUTO || path == PATCH_PATH_GEMM) {
         int64_t units = 0, slabs = 0;

@@ -362,7 +362,9 @@ patch_status patch_group_linear_host(patch_group g, const void* const* X, int64_
  * patch_group_path - the explicit path (GEMV, GEMV_SIMT, GEMM_SINGLE,
  * GEMM_PAIR, GEMM_WIDE or GEMM_WIDE_24) that patch_group_linear would run for this M and
  * requested path; nothing is launched. *out receives the value.
- * Errors: PATCH_ERR_ARG for a NULL group or out, M < 0 or an unknown path.
+ * Errors: PATCH_ERR_ARG for a NULL group or out, M < 0 or an unknown path; for an
+ * 8-bit group also what its product would refuse (PATCH_ERR_SHAPE for an M too
+ * large, PATCH_ERR_UNSUPPORTED for a path without an 8-bit kernel).
  */
 patch_status patch_group_path(patch_group g, int64_t M, int path, int* out);
 

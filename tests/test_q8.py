@@ -638,6 +638,19 @@ def test_memory_of_a_call_belongs_to_its_stream(hsg, raw, monkeypatch):
         del fresh
 
 
+def test_path_of_extreme_sizes(hsg):
+    w = Weight(hsg, 512, 512, seed=1)
+    group = hsg.LinearGroupQ8([w.lin])
+    for M in (0, 1, 64, 65, 10**6, 2**30 - 1):
+        for path in (hsg.PATH_AUTO, hsg.PATH_GEMM):
+            kernels = {hsg.PATH_GEMM_SINGLE, hsg.PATH_GEMM_WIDE} | ({hsg.PATH_GEMV} if path == hsg.PATH_AUTO else set())
+            assert group.path(M, path) in kernels
+    for M in (2**30, 2**31, 2**62):
+        with pytest.raises(hsg.PatchError) as e:
+            group.path(M)
+        assert hsg.STATUS_NAMES[e.value.status] == "PATCH_ERR_SHAPE"
+
+
 def test_handles_come_and_go(hsg):
     before = None
     for i in range(6):
