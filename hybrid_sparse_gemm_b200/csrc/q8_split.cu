@@ -315,7 +315,12 @@ __global__ void __launch_bounds__(kThreads, CTAS)
             default: join<8>(base, rank, items, store); break;
         }
     }
-    if (P > 1) cluster_sync();  // no CTA leaves while another may still read its sums
+    // No CTA leaves while another may still read its sums. Nothing has to be visible
+    // after this barrier, and a thread arrives behind the stores that consumed what
+    // it read, so it does not wait for its stores as an arrival with release would:
+    // 16 x 4096 x 4096 4.2 us instead of 4.7, 64 tokens 5.8 and 6.2.
+    if (P > 1)
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 template <int BN, int STAGES, int CTAS, int G, class T>
