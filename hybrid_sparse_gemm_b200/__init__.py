@@ -45,7 +45,6 @@ EXPORTED = ["patch_pack", "patch_linear", "patch_linear_path", "patch_linear_hos
             "patch_pack_q8", "patch_linear_q8", "patch_group_linear_q8", "patch_unpack_q8",
             "patch_quantize_q8", "patch_rmsnorm_q8", "patch_silu_mul_q8", "patch_dequantize_q8"]
 TYPE_BF16, TYPE_FP16, TYPE_FP32, TYPE_INT8 = 0, 1, 2, 3
-_TYPES = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32}
 
 
 class patch_info_t(ctypes.Structure):
@@ -107,12 +106,12 @@ try:
     from . import _binding
 except ImportError as e:
     raise ImportError(f"{os.path.join(_HERE, '_binding.so')} is missing or does not load: build it with "
-                      "`python -m hybrid_sparse_gemm_b200.build`") from e
+                      "`python hybrid_sparse_gemm_b200/build.py`") from e
 _binding.init((torch.bfloat16, torch.float16, torch.float32, torch.int8), torch.cuda.current_device,
               getattr(torch._C, "_cuda_getCurrentRawStream", None),
               tuple(ctypes.cast(getattr(_lib, n), _P).value for n in
                     ("patch_linear_q8", "patch_quantize_q8", "patch_rmsnorm_q8", "patch_silu_mul_q8",
-                     "patch_dequantize_q8")))
+                     "patch_dequantize_q8", "patch_group_linear_q8")))
 
 
 class PatchError(RuntimeError):
@@ -276,18 +275,6 @@ def _on_device(*tensors):
             raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
 
 
-def _rows(name: str, t: torch.Tensor, shape, dtype) -> int:
-    """Row pitch of a 2-D tensor of rows of contiguous elements."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    ld, step = t.stride()
-    if step != 1 and t.shape[1] > 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return ld
-
-
 def _scales(name: str, t: torch.Tensor, n: int):
     if t.dtype is not torch.float32:
         raise TypeError(f"{name} is {t.dtype}, not torch.float32")
@@ -365,8 +352,9 @@ def _empty(shape, dtype, device, stream):
 def _codes_like(x: torch.Tensor, stream):
     """Fresh (codes, scales) for the rows of x; the codes' pitch suits the products."""
     M, K = x.shape
-    q = _empty((M, (K + 15) // 16 * 16), torch.int8, x.device, stream)[:, :K]
-    return q, _empty(M, torch.float32, x.device, stream)
+    pitch = (K + 15) // 16 * 16
+    q = _empty((M, pitch), torch.int8, x.device, stream)
+    return q if pitch == K else q[:, :K], _empty(M, torch.float32, x.device, stream)
 
 
 class LinearGroup:
@@ -546,6 +534,7 @@ class LinearGroupQ8:
         g = _P()
         _check(_lib.patch_group_create(arr, len(self.linears), ctypes.byref(g)))
         self.handle = g.value
+        self._shapes = tuple(d for l in self.linears for d in (l.N, l.K))
 
     def __call__(self, Xs, x_scales, outs=None, out_dtype: torch.dtype = torch.bfloat16, path: int = PATH_AUTO,
                  stream=None):
@@ -553,22 +542,13 @@ class LinearGroupQ8:
         a list with one per member."""
         n = len(self.linears)
         if isinstance(Xs, torch.Tensor):
-            Xs, x_scales = [Xs] * n, [x_scales] * n
+            Xs, x_scales = (Xs,) * n, (x_scales,) * n
         if len(Xs) != n or len(x_scales) != n or (outs is not None and len(outs) != n):
             raise ValueError(f"the group has {n} members")
-        M = Xs[0].shape[0]
         if outs is None:
-            outs = [_empty((M, l.N), out_dtype, Xs[0].device, stream) for l in self.linears]
-        ldx, ldy = (_I64 * n)(), (_I64 * n)()
-        for i, l in enumerate(self.linears):
-            ldx[i] = _rows(f"X {i}", Xs[i], (M, l.K), torch.int8)
-            ldy[i] = _rows(f"out {i}", outs[i], (M, l.N), outs[0].dtype)
-            _scales(f"x_scale {i}", x_scales[i], M)
-        _on_device(*Xs, *x_scales, *outs)
-        _check(_lib.patch_group_linear_q8(self.handle, (_P * n)(*[x.data_ptr() for x in Xs]), ldx,
-                                          (_P * n)(*[x.data_ptr() for x in x_scales]), M,
-                                          (_P * n)(*[y.data_ptr() for y in outs]), ldy, _TYPES[outs[0].dtype], path,
-                                          _stream(stream)))
+            M, device = Xs[0].shape[0], Xs[0].device
+            outs = [_empty((M, N), out_dtype, device, stream) for N in self._shapes[::2]]
+        _check(_binding.group_linear_q8(self.handle, self._shapes, tuple(Xs), tuple(x_scales), tuple(outs), path, stream))
         return outs
 
     def quantize(self, x, outs=None, path: int = PATH_AUTO, stream=None):

@@ -20,6 +20,7 @@ static PyObject *g_dtype[4];                       /* by patch_dtype */
 static PyObject *g_device, *g_stream;
 static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device;
 static __typeof__(&patch_linear_q8) f_linear;
+static __typeof__(&patch_group_linear_q8) f_group;
 static __typeof__(&patch_quantize_q8) f_quantize;
 static __typeof__(&patch_rmsnorm_q8) f_rmsnorm;
 static __typeof__(&patch_silu_mul_q8) f_silu_mul;
@@ -180,6 +181,58 @@ static PyObject *linear_q8(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     CALL(f_linear(h, x.p, x.ld, s.p, x.rows, y.p, y.ld, y.type, (int)path, stream));
 }
 
+/*
+ * group_linear_q8(handle, (N0, K0, N1, K1, ...), Xs, x_scales, outs, path, stream),
+ * the operands in tuples; one that several members share is looked at once
+ */
+enum { kMembers = 8 };
+static PyObject *group_linear_q8(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    const void *xp[kMembers], *sp[kMembers];
+    void *yp[kMembers], *stream;
+    int64_t ldx[kMembers], ldy[kMembers];
+    Mat x = {0}, s = {0}, y = {0};
+    int type = -1;
+    int64_t M = -1;
+    long dev;
+    (void)self;
+    if (count(n, 7)) return NULL;
+    void *h = PyLong_AsVoidPtr(a[0]);
+    const long path = PyLong_AsLong(a[5]);
+    if (PyErr_Occurred()) return NULL;
+    for (int i = 1; i < 5; ++i)
+        if (!PyTuple_Check(a[i])) {
+            PyErr_SetString(PyExc_TypeError, "shapes, Xs, x_scales and outs must be tuples");
+            return NULL;
+        }
+    const Py_ssize_t g = PyTuple_GET_SIZE(a[2]);
+    if (g < 1 || g > kMembers || PyTuple_GET_SIZE(a[1]) != 2 * g || PyTuple_GET_SIZE(a[3]) != g ||
+        PyTuple_GET_SIZE(a[4]) != g) {
+        PyErr_Format(PyExc_ValueError, "one X, x_scale and out for each of 1 to %d members", (int)kMembers);
+        return NULL;
+    }
+    if (current_device(PyTuple_GET_ITEM(a[2], 0), &dev) || stream_of(a[6], dev, &stream)) return NULL;
+    for (Py_ssize_t l = 0; l < g; ++l) {
+        int64_t N, K;
+        PyObject *xo = PyTuple_GET_ITEM(a[2], l), *so = PyTuple_GET_ITEM(a[3], l);
+        if (as_i64(PyTuple_GET_ITEM(a[1], 2 * l), &N) || as_i64(PyTuple_GET_ITEM(a[1], 2 * l + 1), &K)) return NULL;
+        if ((l == 0 || xo != PyTuple_GET_ITEM(a[2], l - 1)) && matrix(xo, "X", 2, dev, &x)) return NULL;
+        if ((l == 0 || so != PyTuple_GET_ITEM(a[3], l - 1)) && matrix(so, "x_scale", 1, dev, &s)) return NULL;
+        if (matrix(PyTuple_GET_ITEM(a[4], l), "out", 2, dev, &y) || number_type(&y, "out")) return NULL;
+        if (l == 0) {
+            M = x.rows;
+            type = y.type;
+        }
+        if (want(&x, "X", M, K, PATCH_INT8) || want(&s, "x_scale", 1, M, PATCH_FP32) || want(&y, "out", M, N, type))
+            return NULL;
+        xp[l] = x.p;
+        ldx[l] = x.ld;
+        sp[l] = s.p;
+        yp[l] = y.p;
+        ldy[l] = y.ld;
+    }
+    CALL(f_group(h, (const int8_t *const *)xp, ldx, (const float *const *)sp, M, yp, ldy, type, (int)path, stream));
+}
+
 /* quantize_q8(x, q, scale, stream) */
 static PyObject *quantize_q8(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     Mat x, q, s;
@@ -249,10 +302,10 @@ static PyObject *dequantize_q8(PyObject *self, PyObject *const *a, Py_ssize_t n)
 /* init((dtypes by patch_dtype), current_device, current_raw_stream, (addresses)) */
 static PyObject *init(PyObject *self, PyObject *args) {
     PyObject *dtypes, *device, *stream;
-    unsigned long long f[5];
+    unsigned long long f[6];
     (void)self;
-    if (!PyArg_ParseTuple(args, "O!OO(KKKKK)", &PyTuple_Type, &dtypes, &device, &stream, &f[0], &f[1], &f[2], &f[3],
-                          &f[4]))
+    if (!PyArg_ParseTuple(args, "O!OO(KKKKKK)", &PyTuple_Type, &dtypes, &device, &stream, &f[0], &f[1], &f[2], &f[3],
+                          &f[4], &f[5]))
         return NULL;
     if (PyTuple_GET_SIZE(dtypes) != 4) {
         PyErr_SetString(PyExc_ValueError, "four dtypes");
@@ -266,12 +319,14 @@ static PyObject *init(PyObject *self, PyObject *args) {
     f_rmsnorm = (__typeof__(f_rmsnorm))(uintptr_t)f[2];
     f_silu_mul = (__typeof__(f_silu_mul))(uintptr_t)f[3];
     f_dequantize = (__typeof__(f_dequantize))(uintptr_t)f[4];
+    f_group = (__typeof__(f_group))(uintptr_t)f[5];
     Py_RETURN_NONE;
 }
 
 static PyMethodDef methods[] = {
     {"init", init, METH_VARARGS, NULL},
     {"linear_q8", (PyCFunction)(void (*)(void))linear_q8, METH_FASTCALL, NULL},
+    {"group_linear_q8", (PyCFunction)(void (*)(void))group_linear_q8, METH_FASTCALL, NULL},
     {"quantize_q8", (PyCFunction)(void (*)(void))quantize_q8, METH_FASTCALL, NULL},
     {"rmsnorm_q8", (PyCFunction)(void (*)(void))rmsnorm_q8, METH_FASTCALL, NULL},
     {"silu_mul_q8", (PyCFunction)(void (*)(void))silu_mul_q8, METH_FASTCALL, NULL},
