@@ -638,6 +638,32 @@ def test_memory_of_a_call_belongs_to_its_stream(hsg, raw, monkeypatch):
         del fresh
 
 
+def test_capture_with_the_stream_named(hsg):
+    """The memory of a captured call belongs to the graph, whether its stream is named or current."""
+    M, K = 20, 512
+    w = Weight(hsg, 512, K, frac=0.5, seed=4)
+    group = hsg.LinearGroupQ8([w.lin])
+    x = rows(gen("cap"), M, K, torch.bfloat16).contiguous()
+    gamma = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    want, h = group.norm(x, gamma, 1e-5, x)
+    want = group.silu_mul(want[0], h)[0].clone()
+    torch.cuda.synchronize()
+    for raw in (False, True):
+        side = torch.cuda.Stream()
+        name = side.cuda_stream if raw else side
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            y, h = group.norm(x, gamma, 1e-5, x, stream=name)
+            y = group.silu_mul(y[0], h, stream=name)[0]
+        junk = [torch.full((M * K * 4,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        for _ in range(2):
+            y.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
+        assert all(bool((j == 7).all()) for j in junk)
+
+
 def test_path_of_extreme_sizes(hsg):
     w = Weight(hsg, 512, 512, seed=1)
     group = hsg.LinearGroupQ8([w.lin])
