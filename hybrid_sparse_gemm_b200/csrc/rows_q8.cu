@@ -22,6 +22,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "q8.cuh"
 
@@ -138,18 +139,48 @@ __device__ __forceinline__ void store_any(T* row, int e, int K, const float* v) 
     }
 }
 
-// round(v * inv), ties to even, as the low byte: the product is rounded once,
-// into the mantissa of 1.5 * 2^23 (|v * inv| is at most 127 and a little).
-__device__ __forceinline__ uint32_t code_bits(float v, float inv) {
-    return __float_as_uint(__fmaf_rn(v, inv, 12582912.f));
+// What turns a row's values into codes: round(v * pre * up / step).
+struct RowScale {
+    float pre, up;  // both 1 unless the scale is very small
+    float step, inv;  // inv: 1 / step, rounded
+    bool finite;
+};
+
+// round(v / step), ties to even, as the low byte, the quotient being the one of an
+// fp32 division: one Newton step on v * inv gives it (P. Markstein, IBM J. Res.
+// Dev. 34, 1990), a sum with 1.5 * 2^23 rounds it into the low bits (it is at most
+// 127). Tried on the CPU against rint(v / step) at every tie n + 1/2, n < 128, with
+// every mantissa of the step and the nine values around the tie: no code differs;
+// with the product v * inv alone, 6 in 100 of them do. Quotients near a tie are not
+// rare, since half a row's maximum lies at 63.5. The remainder v - q * step has to be
+// representable: row_scale lifts steps below 2^-64.
+__device__ __forceinline__ uint32_t code_bits(float v, const RowScale& s) {
+    const float q = __fmul_rn(v, s.inv);
+    return __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-q, s.step, v), s.inv, q), 12582912.f));
 }
-__device__ __forceinline__ uint2 codes8(const float* v, float inv, bool finite) {
+// The same for two values at once: half the instructions.
+__device__ __forceinline__ uint2 code_bits2(float v0, float v1, const RowScale& s) {
+    uint32_t a, b;
+    asm("{\n\t.reg .b64 v, q, r, i, d, m;\n\t"
+        "mov.b64 v, {%2, %3};\n\t"
+        "mov.b64 i, {%4, %4};\n\t"
+        "mov.b64 d, {%5, %5};\n\t"
+        "mov.b64 m, {%6, %6};\n\t"
+        "mul.rn.f32x2 q, v, i;\n\t"
+        "fma.rn.f32x2 r, q, d, v;\n\t"  // d: -step, so that (-q) * step = q * d
+        "fma.rn.f32x2 q, r, i, q;\n\t"
+        "add.rn.f32x2 q, q, m;\n\t"
+        "mov.b64 {%0, %1}, q;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "f"(v0), "f"(v1), "f"(s.inv), "f"(-s.step), "f"(12582912.f));
+    return make_uint2(a, b);
+}
+__device__ __forceinline__ uint2 codes8(const float* v, const RowScale& s) {
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint32_t lo = __byte_perm(code_bits(v[4 * i], inv), code_bits(v[4 * i + 1], inv), 0x0040);
-        const uint32_t hi = __byte_perm(code_bits(v[4 * i + 2], inv), code_bits(v[4 * i + 3], inv), 0x0040);
-        w[i] = finite ? __byte_perm(lo, hi, 0x5410) : 0u;
+        const uint2 a = code_bits2(v[4 * i], v[4 * i + 1], s), b = code_bits2(v[4 * i + 2], v[4 * i + 3], s);
+        w[i] = s.finite ? __byte_perm(__byte_perm(a.x, a.y, 0x0040), __byte_perm(b.x, b.y, 0x0040), 0x5410) : 0u;
     }
     return make_uint2(w[0], w[1]);
 }
@@ -285,10 +316,6 @@ __device__ __forceinline__ float combine_one(T& x, T r, T gamma, float& ss) {
     return v;
 }
 
-struct RowScale {
-    float pre, inv;  // codes round(v * pre * inv)
-    bool finite;
-};
 // Reduces the row's maximum and sum over the blockDim.x threads that hold it,
 // and writes its scale. s: 64 words, another set for the row after this one.
 template <int MODE>
@@ -319,19 +346,25 @@ __device__ __forceinline__ RowScale row_scale(const RowArgs& a, int64_t row, flo
     RowScale x;
     x.finite = top < 0x7F800000u;
     const float most = __uint_as_float(top);
-    float step = most / 127.f, scale = step;
-    x.pre = 1.f;
+    float scale = most / 127.f;
+    x.step = scale;
+    x.pre = x.up = 1.f;
     if (is_norm(MODE)) {
         const float r = rsqrtf(ss / (float)a.K + a.eps);
         scale = most * r / 127.f;
         x.finite = x.finite && ss < INFINITY && scale < INFINITY;
-        if (step < kMinScale || scale < kMinScale) {
+        if (x.step < kMinScale || scale < kMinScale) {
             x.pre = r;
-            step = fmaxf(scale, kMinScale);
+            x.step = scale;
         }
     }
     scale = fmaxf(scale, kMinScale);
-    x.inv = 1.f / fmaxf(step, kMinScale);  // at most 2^126
+    x.step = fmaxf(x.step, kMinScale);
+    if (x.step < 0x1p-64f) {  // both lifted by the same power of two
+        x.up = 0x1p62f;
+        x.step *= x.up;
+    }
+    x.inv = 1.f / x.step;
     if (threadIdx.x == 0) a.scale[row] = x.finite ? scale : __uint_as_float(0x7FC00000u);
     return x;
 }
@@ -357,13 +390,21 @@ __device__ __forceinline__ void look(const Raw<__half>& x, float& top) {
 __device__ __forceinline__ void look(const Raw<float>& x, float& top) {
     look(reinterpret_cast<const float*>(x.w), top);
 }
-template <int MODE>
+// all(lifted) makes a row's codes: in one go where the values are taken as they
+// are, which nearly all rows' are. (A branch at every group keeps the compiler from
+// mixing the groups' instructions.)
+template <bool LIFTED>
 __device__ __forceinline__ uint2 codes_of(float* v, const RowScale& s) {
-    if (is_norm(MODE) && s.pre != 1.f) {
+    if (LIFTED) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= s.pre;
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * s.pre * s.up;
     }
-    return codes8(v, s.inv, s.finite);
+    return codes8(v, s);
+}
+template <class All>
+__device__ __forceinline__ void make_codes(const RowScale& s, All all) {
+    if (s.pre == 1.f && s.up == 1.f) all(std::false_type());
+    else all(std::true_type());
 }
 
 // blockDim.x threads per row (one warp, then blockDim.y rows at a time; or the
@@ -422,12 +463,14 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const RowArgs a) {
         if (row + step < a.M) fetch(row + step);
         const RowScale sc = row_scale<MODE>(a, row, top, ss, s[turn]);
         int8_t* q = a.q + row * a.ldq;
+        make_codes(sc, [&](auto lifted) {
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            if constexpr (kPacked) unpack(now[i], v[0]);
-            const uint2 c = codes_of<MODE>(v[kPacked ? 0 : i], sc);
-            if (group(i) < a.K) *reinterpret_cast<uint2*>(q + group(i)) = c;
-        }
+            for (int i = 0; i < ITEMS; ++i) {
+                if constexpr (kPacked) unpack(now[i], v[0]);
+                const uint2 c = codes_of<lifted>(v[kPacked ? 0 : i], sc);
+                if (group(i) < a.K) *reinterpret_cast<uint2*>(q + group(i)) = c;
+            }
+        });
     }
 }
 
@@ -535,11 +578,13 @@ __global__ void __launch_bounds__(THREADS) rows_edge_kernel(const RowArgs a) {
         int8_t* q = a.q + row * a.ldq + p.head;
         const int off = (int)(reinterpret_cast<uintptr_t>(q) & 7u);  // of every group
         uint2 c[ITEMS];
+        make_codes(sc, [&](auto lifted) {
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            if constexpr (kPacked) unpack(now[i], v[0]);
-            c[i] = codes_of<MODE>(v[kPacked ? 0 : i], sc);
-        }
+            for (int i = 0; i < ITEMS; ++i) {
+                if constexpr (kPacked) unpack(now[i], v[0]);
+                c[i] = codes_of<lifted>(v[kPacked ? 0 : i], sc);
+            }
+        });
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             const int g = first + 32 * i;
@@ -558,8 +603,8 @@ __global__ void __launch_bounds__(THREADS) rows_edge_kernel(const RowArgs a) {
             }
         }
         if (p.beside >= 0) {
-            if (is_norm(MODE) && sc.pre != 1.f) bv *= sc.pre;
-            a.q[row * a.ldq + p.beside] = sc.finite ? (int8_t)(code_bits(bv, sc.inv) & 0xFFu) : (int8_t)0;
+            bv = bv * sc.pre * sc.up;
+            a.q[row * a.ldq + p.beside] = sc.finite ? (int8_t)(code_bits(bv, sc) & 0xFFu) : (int8_t)0;
         }
     }
 }
@@ -606,9 +651,11 @@ __global__ void __launch_bounds__(512) rows_any_kernel(const RowArgs a) {
                 look(v[i], top);
             }
             const RowScale sc = row_scale<MODE>(a, row, top, ss, s[turn]);
+            make_codes(sc, [&](auto lifted) {
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i)
-                store_codes_any(a.q + row * a.ldq, (i * n + (int)threadIdx.x) * 8 - off, a.K, codes_of<MODE>(v[i], sc));
+                for (int i = 0; i < ITEMS; ++i)
+                    store_codes_any(a.q + row * a.ldq, (i * n + (int)threadIdx.x) * 8 - off, a.K, codes_of<lifted>(v[i], sc));
+            });
         } else {
             // whole warps take part to the end, for the exchange between lanes
             const int64_t end = ((int64_t)a.K + off + 8 * n - 1) / (8 * n) * (8 * n);
@@ -620,7 +667,7 @@ __global__ void __launch_bounds__(512) rows_any_kernel(const RowArgs a) {
             const RowScale sc = row_scale<MODE>(a, row, top, ss, s[turn]);
             for (int64_t e = (int64_t)threadIdx.x * 8; e < end; e += 8 * n) {
                 group((int)e - off, v, unused, true);
-                store_codes_any(a.q + row * a.ldq, (int)e - off, a.K, codes_of<MODE>(v, sc));
+                store_codes_any(a.q + row * a.ldq, (int)e - off, a.K, codes_of<true>(v, sc));
             }
         }
     }

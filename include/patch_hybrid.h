@@ -432,7 +432,8 @@ patch_status patch_selftest_wait(void* stream);
  *
  *     scale = max(max_k |y[k]| / 127, 2^-126)     code[k] = round(y[k] / scale)
  *
- * (ties to even; codes in -127..127), and stands for code * scale. Activations
+ * (both quotients are fp32 divisions, rounded once; ties to even; codes in
+ * -127..127), and stands for code * scale. Activations
  * have one scale per token, weights one per output channel. A row that holds a
  * NaN or an infinity, or whose norm's sum of squares overflows fp32, gets the
  * scale NaN and zero codes: what is computed from it is NaN.
@@ -520,7 +521,11 @@ patch_status patch_quantize_q8(const void* x, int64_t ldx, int type, int64_t M, 
  *   residual, residual_out  dev, M rows of K, or both NULL. residual_out may be
  *          x or residual itself (same pointer and pitch).
  *   gamma  dev, K elements of `type`.
- * The sum of squares and the norm are fp32; they see the rounded h.
+ * The sum of squares and the norm are fp32; they see the rounded h. The norm is a
+ * factor common to a row's values and its scale: code[k] = round(g[k] / (max|g| / 127))
+ * with g = h * gamma in fp32, so that codes do not depend on the order of the sum.
+ * (Where max|g| / 127 or the scale is below 2^-126, the codes are those of the
+ * normalised values.)
  */
 patch_status patch_rmsnorm_q8(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* residual_out,
                               int64_t ldo, const void* gamma, int type, float eps, int64_t M, int64_t K, int8_t* q,
