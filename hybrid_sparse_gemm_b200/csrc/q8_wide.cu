@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t ldy = L.ldy;
             for (int i = lane; i < cols; i += 32) sx[i] = tok0 + i < a.M ? L.x_scale[tok0 + i] : 0.f;
             __syncwarp();
-            if (!mbar_wait(&acc_full[h], t & 1, abort_flag)) {
+            // (the lanes may see a limit or the abort flag at different times)
+            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[h], t & 1, abort_flag))) {
                 if (lane == 0) raise();
                 break;
             }
