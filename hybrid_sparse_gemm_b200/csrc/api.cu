@@ -1078,6 +1078,7 @@ patch_status run_q8_split(patch_group g, const Q8Call& c, int path, cudaStream_t
     a.n_tok = plan.n_tok;
     a.MB = plan.mb;
     a.P = plan.P;
+    a.zero = 0;
     a.M = (int)c.M;
     a.n = g->n;
     a.status = g->status_dev;

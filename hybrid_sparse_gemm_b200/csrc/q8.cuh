@@ -69,6 +69,7 @@ struct Q8SplitArgs {
     int MB;     // token tiles
     int n_tok;  // tokens per tile, a multiple of 16
     int P;      // CTAs per unit
+    uint32_t zero;  // 0 (see the kernel's join)
 };
 // The kernel's forms: tokens per unit (n_tok at most), pipeline stages, CTAs
 // resident per SM. They share the SM's shared memory. One CTA with a deep pipeline

@@ -6,6 +6,9 @@ the lanes of a warp may see a time limit or the abort flag at different times. S
 
 - what a wait returned is agreed on by the warp before the warp acts on it;
 - lanes that ran a loop of their own meet again before a barrier of the cluster.
+
+A CTA may leave once the others have read its shared memory. An arrival without
+release says nothing about the reads before it, so it has to depend on their values.
 """
 import os
 import re
@@ -39,3 +42,12 @@ def test_warps_meet_before_a_cluster_barrier():
                 f"{os.path.basename(p)}:{code.count(chr(10), 0, m.start()) + 1}"
             seen += 1
     assert seen >= 4
+
+
+def test_an_arrival_that_orders_nothing_depends_on_what_was_read():
+    for p in SOURCES:
+        code = _code(p)
+        for m in re.finditer(r"arrive\.relaxed", code):
+            near = code[max(0, m.start() - 400):m.end() + 200]
+            assert "@p barrier.cluster.arrive.relaxed" in near and "seen & zero" in near, \
+                f"{os.path.basename(p)}:{code.count(chr(10), 0, m.start()) + 1}"
