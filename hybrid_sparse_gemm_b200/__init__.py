@@ -314,6 +314,15 @@ def patch_linear_q8(h: int, X: torch.Tensor, x_scale: torch.Tensor, Y: torch.Ten
 
 
 def patch_unpack_q8(h: int, W: torch.Tensor, w_scale: torch.Tensor, stream=None):
+    """The masked codes W [N,K] (int8) and the channel scales w_scale [N] (fp32) of a handle."""
+    _check(_lib.patch_linear_q8(h, None, 0, None, 0, None, 0, TYPE_BF16, PATH_AUTO, None))  # no tokens: is it an 8-bit handle
+    info = patch_info(h)
+    if W.dtype is not torch.int8:
+        raise TypeError(f"W is {W.dtype}, not torch.int8")
+    if W.shape != (info.N, info.K) or not W.is_contiguous():
+        raise ValueError(f"W must be contiguous {info.N}x{info.K} codes")
+    _scales("w_scale", w_scale, info.N)
+    _on_device(W, w_scale)
     _check(_lib.patch_unpack_q8(h, W.data_ptr(), w_scale.data_ptr(), _stream(stream)))
 
 

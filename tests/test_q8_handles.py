@@ -1,0 +1,47 @@
+"""What the thin calls on an 8-bit handle refuse, and what a handle holds, byte by
+byte. Every refusal is raised before a kernel is launched."""
+import numpy as np
+import pytest
+import torch
+
+import synth
+
+pytestmark = pytest.mark.gpu
+N, K = 384, 448
+
+
+@pytest.fixture(scope="module")
+def hsg():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    import hybrid_sparse_gemm_b200 as m
+    return m
+
+
+def pack(hsg, n=N, k=K, R=128, C=64, frac=0.6):
+    p = synth.make_problem(n, k, 0, R=R, C=C, frac=frac, seed=17, device="cuda")
+    g = synth.generator("cuda", "handles", n, k, R, C)
+    W = torch.randint(-128, 128, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    scale = torch.rand(n, generator=g, device="cuda") + 0.5
+    lin = hsg.PackedLinearQ8.pack(W, p.bits, p.flags.cpu(), R, C, w_scale=scale)
+    return lin, W * p.keep, scale
+
+
+def test_unpack_writes_into_fitting_tensors_only(hsg):
+    lin, masked, scale = pack(hsg)
+    W, s = torch.empty(N, K, dtype=torch.int8, device="cuda"), torch.empty(N, device="cuda")
+    for bad in (lambda: hsg.patch_unpack_q8(lin.handle, W[:-1], s), lambda: hsg.patch_unpack_q8(lin.handle, W[:, :-64], s),
+                lambda: hsg.patch_unpack_q8(lin.handle, W.view(-1), s), lambda: hsg.patch_unpack_q8(lin.handle, W, s[:-1]),
+                lambda: hsg.patch_unpack_q8(lin.handle, torch.empty(K, N, dtype=torch.int8, device="cuda").t(), s),
+                lambda: hsg.patch_unpack_q8(lin.handle, torch.empty(N, K + 16, dtype=torch.int8, device="cuda")[:, :K], s),
+                lambda: hsg.patch_unpack_q8(lin.handle, W, torch.empty(2 * N, device="cuda")[::2]),
+                lambda: hsg.patch_unpack_q8(lin.handle, W.cpu(), s), lambda: hsg.patch_unpack_q8(lin.handle, W, s.cpu())):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: hsg.patch_unpack_q8(lin.handle, W.view(torch.uint8), s),
+                lambda: hsg.patch_unpack_q8(lin.handle, W.to(torch.bfloat16), s),
+                lambda: hsg.patch_unpack_q8(lin.handle, W, s.double())):
+        with pytest.raises(TypeError):
+            bad()
+    hsg.patch_unpack_q8(lin.handle, W, s)
+    assert torch.equal(W, masked) and torch.equal(s, scale)
