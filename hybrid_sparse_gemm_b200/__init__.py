@@ -310,7 +310,13 @@ def patch_pack_q8(W: torch.Tensor, mask_bits: torch.Tensor, tile_flags, tile_row
 
 def patch_linear_q8(h: int, X: torch.Tensor, x_scale: torch.Tensor, Y: torch.Tensor, path: int = PATH_AUTO, stream=None):
     """Y [M,N] (bf16, fp16 or fp32) from the codes X [M,K] and their scales [M]."""
-    _check(_binding.linear_q8(h, Y.shape[1], X.shape[1], X, x_scale, Y, path, stream))
+    for t in (X, x_scale, Y):
+        if not t.is_cuda:
+            raise ValueError(f"tensor on {t.device}, not on the current CUDA device")
+    info = patch_info(h)
+    if X.dim() == 2 and Y.dim() == 2 and (X.shape[1] != info.K or Y.shape[1] != info.N):
+        raise PatchError(2, f"X has {X.shape[1]} columns and Y {Y.shape[1]}, the weight is {info.N}x{info.K}")
+    _check(_binding.linear_q8(h, info.N, info.K, X, x_scale, Y, path, stream))
 
 
 def patch_unpack_q8(h: int, W: torch.Tensor, w_scale: torch.Tensor, stream=None):

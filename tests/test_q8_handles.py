@@ -45,3 +45,23 @@ def test_unpack_writes_into_fitting_tensors_only(hsg):
             bad()
     hsg.patch_unpack_q8(lin.handle, W, s)
     assert torch.equal(W, masked) and torch.equal(s, scale)
+
+
+@pytest.mark.parametrize("M", [1, 4, 200])
+def test_product_of_another_shape(hsg, M):
+    """One row has no pitch to be checked by: the columns decide."""
+    lin, masked, scale = pack(hsg)
+    x, sx = torch.ones(M, K, dtype=torch.int8, device="cuda"), torch.ones(M, device="cuda")
+    y = torch.empty(M, N, device="cuda")
+    for a, b in ((x[:, :256].contiguous(), y), (x, y[:, :128].contiguous()), (x.new_ones(M, K + 64), y),
+                 (x, y.new_empty(M, N + 128)), (x.new_ones(M, N), y.new_empty(M, K))):
+        with pytest.raises(hsg.PatchError) as e:
+            hsg.patch_linear_q8(lin.handle, a, sx, b)
+        assert hsg.STATUS_NAMES[e.value.status] == "PATCH_ERR_SHAPE"
+    for a, b in ((x[0], y), (x, y[0])):
+        with pytest.raises(TypeError):
+            hsg.patch_linear_q8(lin.handle, a, sx, b)
+    hsg.patch_linear_q8(lin.handle, x, sx, y)
+    # whole numbers below 2^24 times one scale: the product's rounding alone
+    want = masked.double().sum(1) * scale.double()
+    assert ((y.double() - want).abs() <= want.abs() * 1.01 * 2.0 ** -24).all()
