@@ -249,7 +249,8 @@ def patch_copy_packed(h: int):
     """(packed bytes as a uint8 numpy array, (slab, meta, gemm) uint32 tables)."""
     import numpy as np
     info = patch_info(h)
-    ns, nm, ng = _table_sizes(int(info.N), int(info.K))
+    ns = ng = int(info.slabs_total)
+    nm = int(info.N) // 128 * ((int(info.K) + 127) // 128)  # 128 columns a block, of bf16 weights and of 8-bit codes
     packed = np.empty(int(info.packed_bytes), np.uint8)
     slab, meta, gemm = np.empty(ns, np.uint32), np.empty(nm, np.uint32), np.empty(ng, np.uint32)
     _check(_lib.patch_copy_packed(h, packed.ctypes.data, packed.size, slab.ctypes.data, ns,

@@ -93,7 +93,8 @@ typedef struct {
     int32_t tile_rows, tile_cols;
     int64_t tiles_total;        /* (N/tile_rows) * (K/tile_cols) */
     int64_t tiles_sparse;       /* tiles flagged 2:4 */
-    int64_t slabs_total;        /* (N/128) * (K/64) storage slabs */
+    int64_t slabs_total;        /* (N/128) * (K/64) storage slabs; of 8-bit codes
+                                   (N/128) * ceil(K/128) */
     int64_t slabs_sparse;       /* slabs stored compressed */
     int64_t slabs_pair_sparse;  /* slabs the CTA-pair kernel runs on the sparse MMA */
     int64_t meta_blocks;        /* 2048-byte metadata blocks */
@@ -383,7 +384,8 @@ patch_status patch_info(patch_handle h, patch_info_t* info);
  *   packed_host  host, packed_cap bytes (>= info.packed_bytes), or NULL.
  *   slab_host, meta_host, gemm_host  host tables with their capacities in
  *                entries, or NULL. A too-small buffer gives PATCH_ERR_ARG.
- * With S = N/128 strips, KB = K/64 slabs and KC = ceil(KB/2) chunks:
+ * With S = N/128 strips, KB = K/64 slabs and KC = ceil(KB/2) chunks (8-bit codes:
+ * see patch_pack_q8):
  *   slab[s*KB+b] = (offset/16)<<2 | first<<1 | sparse: the slab's own record,
  *     a 16384-byte dense block or 8192 bytes of kept 2:4 values; first marks
  *     the first 2:4 slab of its 128-column chunk.
@@ -465,7 +467,8 @@ patch_status patch_selftest_wait(void* stream);
  *            codes are exact.
  * The handle works with patch_linear_q8, patch_unpack_q8, patch_info,
  * patch_copy_packed (its slabs are 128 columns wide: KB = KC = ceil(K/128); a 2:4
- * record is 8192 bytes of codes and its 2048-byte metadata block), patch_check,
+ * record is 8192 bytes of codes and its 2048-byte metadata block, 16 bytes a row,
+ * the two 2-bit positions of group g of four columns at bit 4g), patch_check,
  * patch_free, patch_group_create (with other 8-bit handles) and
  * patch_group_path; the bf16 calls refuse it (PATCH_ERR_ARG). A bf16 channel
  * that keeps a NaN or an infinity gives PATCH_ERR_ARG.

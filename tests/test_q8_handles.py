@@ -65,3 +65,45 @@ def test_product_of_another_shape(hsg, M):
     # whole numbers below 2^24 times one scale: the product's rounding alone
     want = masked.double().sum(1) * scale.double()
     assert ((y.double() - want).abs() <= want.abs() * 1.01 * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("n,k,R,C,frac", [(384, 448, 128, 64, 0.6), (256, 384, 128, 128, 0.5), (128, 64, 64, 64, 1.0),
+                                          (640, 320, 64, 64, 0.8), (256, 128, 128, 128, 0.0)])
+def test_packed_bytes(hsg, n, k, R, C, frac):
+    """Each record, decoded by the header's layout: 128 x 128 codes in 128-byte
+    swizzled rows, or 64 kept codes a row in 64-byte swizzled ones and 16 bytes of
+    position codes a row behind them."""
+    lin, masked, _ = pack(hsg, n, k, R, C, frac)
+    info = lin.info()
+    packed, (slab, meta, gemm) = hsg.patch_copy_packed(lin.handle)
+    S, KB = n // 128, (k + 127) // 128
+    assert info.slabs_total == S * KB == slab.size == meta.size == gemm.size and packed.size == info.packed_bytes
+    assert int((slab & 1).sum()) == info.slabs_sparse and int((gemm & 1).sum()) == info.slabs_pair_sparse
+    want = np.zeros((n, KB * 128), np.int8)
+    want[:, :k] = masked.cpu().numpy()
+
+    def record(entry):
+        at = int(entry >> 2) * 16
+        got = np.zeros((128, 128), np.int8)
+        if not entry & 1:
+            for r in range(128):
+                for c in range(8):
+                    o = at + r * 128 + ((c ^ (r & 7)) << 4)
+                    got[r, 16 * c:16 * c + 16] = packed[o:o + 16].view(np.int8)
+            return got
+        for r in range(128):
+            kept = np.concatenate([packed[o:o + 16] for o in (at + r * 64 + ((c ^ ((r >> 1) & 3)) << 4) for c in range(4))])
+            code = packed[at + 8192 + 16 * r:at + 8192 + 16 * r + 16]
+            for g in range(32):
+                p = (int(code[g // 2]) >> (4 * (g & 1))) & 15
+                assert p & 3 < p >> 2
+                got[r, 4 * g + (p & 3)], got[r, 4 * g + (p >> 2)] = kept.view(np.int8)[2 * g:2 * g + 2]
+        return got
+
+    for s in range(S):
+        for b in range(KB):
+            i = s * KB + b
+            block = want[128 * s:128 * s + 128, 128 * b:128 * b + 128]
+            assert np.array_equal(record(slab[i]), block) and np.array_equal(record(gemm[i]), block)
+            assert meta[i] == ((slab[i] >> 2) + 512 if slab[i] & 1 else 0xFFFFFFFF)
+            assert not (gemm[i] & 1) or slab[i] & 1
