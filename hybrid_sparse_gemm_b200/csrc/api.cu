@@ -1494,7 +1494,10 @@ patch_status pack_weights(const void* W_bf16, bool q8, const float* w_scale, int
     if (cnt[0] != 0)
         return cleanup(fail(PATCH_ERR_MASK, "%llu groups inside 2:4 tiles do not keep exactly two of four", cnt[0]));
     if (cnt[3] != 0)
-        return cleanup(fail(PATCH_ERR_ARG, "%llu output channels keep a NaN or an infinity", cnt[3]));
+        return cleanup(fail(PATCH_ERR_ARG,
+                            w_scale ? "%llu channel scales are negative, infinite or NaN"
+                                    : "%llu output channels keep a NaN or an infinity",
+                            cnt[3]));
     h->desc.packed = h->packed;
     h->desc.slab = h->slab_dev;
     h->desc.meta = h->meta_dev;

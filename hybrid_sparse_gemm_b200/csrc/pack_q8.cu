@@ -112,6 +112,10 @@ __global__ void __launch_bounds__(256) q8_pack_kernel(const Q8PackArgs a) {
     if (threadIdx.x < 3) s_cnt[threadIdx.x] = 0;
     __syncthreads();
     const int s = blockIdx.x / a.KB, b = blockIdx.x % a.KB;
+    if (a.w_int8 && b == 0 && threadIdx.x < kStrip) {
+        const float given = a.w_scale[s * kStrip + threadIdx.x];
+        if (!(given >= 0.f && given < INFINITY)) atomicAdd(&a.counters[3], 1ull);
+    }
     const uint32_t d = a.slab[blockIdx.x];
     uint8_t* base = a.out + slab_offset_bytes(d);
     unsigned long long bad = 0, stray = 0, pruned = 0;

@@ -34,7 +34,7 @@ struct Q8PackArgs {
     const uint8_t* flags;     // tile flags on the device, (N/R) x (K/C)
     const uint32_t* slab;     // per-strip slab table, S x KB
     const uint32_t* gemm;     // CTA-pair slab table, S x KB
-    float* w_scale;           // N channel scales (written for bf16 weights, read back by the pack)
+    float* w_scale;           // N channel scales (written for bf16 weights, checked for int8 codes)
     uint8_t* out;             // packed bytes
     int64_t K;
     int R, C, KB;

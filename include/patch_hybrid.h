@@ -460,8 +460,8 @@ patch_status patch_selftest_wait(void* stream);
  *   W        dev, N*K row-major, 16-byte aligned: bf16 (w_type PATCH_BF16; each
  *            channel is quantised over its kept weights) or int8 codes (w_type
  *            PATCH_INT8). Not retained.
- *   w_scale  dev, N fp32: the channel scales of int8 codes (copied); NULL for
- *            bf16 weights.
+ *   w_scale  dev, N fp32: the channel scales of int8 codes (copied; finite and not
+ *            negative, else PATCH_ERR_ARG); NULL for bf16 weights.
  *   N, K, mask_bits, bitorder, tile_flags, tile_rows, tile_cols, stream, out
  *            as for patch_pack; K <= 131008, so that the int32 sums of any
  *            codes are exact.

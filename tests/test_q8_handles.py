@@ -107,3 +107,18 @@ def test_packed_bytes(hsg, n, k, R, C, frac):
             assert np.array_equal(record(slab[i]), block) and np.array_equal(record(gemm[i]), block)
             assert meta[i] == ((slab[i] >> 2) + 512 if slab[i] & 1 else 0xFFFFFFFF)
             assert not (gemm[i] & 1) or slab[i] & 1
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf"), -1.0, -2.0 ** -140])
+@pytest.mark.parametrize("row", [0, 127, 200, N - 1])
+def test_pack_refuses_given_scales(hsg, bad, row):
+    p = synth.make_problem(N, K, 0, C=64, frac=0.5, seed=1, device="cuda")
+    W, s = torch.ones(N, K, dtype=torch.int8, device="cuda"), torch.ones(N, device="cuda")
+    s[row] = bad
+    with pytest.raises(hsg.PatchError) as e:
+        hsg.PackedLinearQ8.pack(W, p.bits, p.flags.cpu(), 128, 64, w_scale=s)
+    assert hsg.STATUS_NAMES[e.value.status] == "PATCH_ERR_ARG"
+    s[row] = 0.0  # a channel of zeros
+    s[row - 1] = 2.0 ** -140
+    got = hsg.PackedLinearQ8.pack(W, p.bits, p.flags.cpu(), 128, 64, w_scale=s).unpack()[1]
+    assert torch.equal(got, s)
