@@ -102,16 +102,27 @@ for _n in ["patch_pack", "patch_linear", "patch_linear_path", "patch_linear_host
     getattr(_lib, _n).restype = ctypes.c_int
 
 
+class _NoBinding:
+    """In the place of the extension that marshals the 8-bit calls, where it is not
+    built for this interpreter: those calls raise, the others do not need it."""
+
+    def __init__(self, why: ImportError):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{_HERE}/_binding.*.so is missing or does not load: build it with "
+                          "`python hybrid_sparse_gemm_b200/build.py`") from self._why
+
+
 try:
     from . import _binding
+    _binding.init((torch.bfloat16, torch.float16, torch.float32, torch.int8), torch.cuda.current_device,
+                  getattr(torch._C, "_cuda_getCurrentRawStream", None),
+                  tuple(ctypes.cast(getattr(_lib, n), _P).value for n in
+                        ("patch_linear_q8", "patch_quantize_q8", "patch_rmsnorm_q8", "patch_silu_mul_q8",
+                         "patch_dequantize_q8", "patch_group_linear_q8")))
 except ImportError as e:
-    raise ImportError(f"{os.path.join(_HERE, '_binding.so')} is missing or does not load: build it with "
-                      "`python hybrid_sparse_gemm_b200/build.py`") from e
-_binding.init((torch.bfloat16, torch.float16, torch.float32, torch.int8), torch.cuda.current_device,
-              getattr(torch._C, "_cuda_getCurrentRawStream", None),
-              tuple(ctypes.cast(getattr(_lib, n), _P).value for n in
-                    ("patch_linear_q8", "patch_quantize_q8", "patch_rmsnorm_q8", "patch_silu_mul_q8",
-                     "patch_dequantize_q8", "patch_group_linear_q8")))
+    _binding = _NoBinding(e)
 
 
 class PatchError(RuntimeError):

@@ -1,5 +1,6 @@
 """Build libpatch_hybrid.so (the C-ABI library) in-tree with nvcc for sm_100a,
-and _binding.so (the Python argument marshalling of its 8-bit calls) with gcc.
+and _binding.<interpreter>.so (the Python argument marshalling of its 8-bit calls)
+with gcc.
 
     python -m hybrid_sparse_gemm_b200.build [--force]
 """
@@ -14,7 +15,8 @@ import sysconfig
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libpatch_hybrid.so")
-BINDING = os.path.join(HERE, "_binding.so")
+# named for the interpreter it is built for: another one looks for its own
+BINDING = os.path.join(HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 CC = os.environ.get("CC", "gcc")
 
@@ -60,6 +62,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if force or stale(BINDING, [binding] + headers()):
         _run([CC, "-O2", "-Wall", "-shared", "-fPIC", "-I", include, "-I", sysconfig.get_paths()["include"], binding],
              BINDING, CC, verbose)
+    untagged = os.path.join(HERE, "_binding.so")  # of an earlier build: any interpreter would load it
+    if os.path.exists(untagged) and untagged != BINDING:
+        os.remove(untagged)
     return LIB
 
 
