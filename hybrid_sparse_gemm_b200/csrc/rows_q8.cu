@@ -5,8 +5,10 @@
 // round(y / s), ties to even. One reduction per row is enough: with
 // y = h * gamma / rms(h), max|y| = max|h * gamma| / rms(h), so the sum of
 // squares and the maximum are reduced together. The row stays in registers
-// between the reduction and the codes, so every input byte is read once.
-// All sums are fp32. A row that holds a NaN or an infinity (or whose sum of
+// between the reduction and the codes, so every input byte is read once; rows of
+// more than 16384 elements, and operands of more than about 8176 that lie at
+// different offsets from their 16-byte boundaries, are read a second time for the
+// codes. All sums are fp32. A row that holds a NaN or an infinity (or whose sum of
 // squares overflows) gets the scale NaN and zero codes, so that a product
 // over it is NaN instead of silently wrong.
 //
@@ -66,16 +68,6 @@ __device__ __forceinline__ void unpack(const Raw<T>& r, float* v) {
     const T* e = reinterpret_cast<const T*>(r.w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = to_float(e[i]);
-}
-
-template <class T>
-__device__ __forceinline__ void store_raw(T* p, const float* v) {
-    Raw<T> r;
-    T* e = reinterpret_cast<T*>(r.w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = from_float<T>(v[i]);
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
 }
 
 // Words w[0 .. N) shifted down by `bytes` (0..15, the same in a warp), from N + 4 words.
@@ -785,8 +777,9 @@ cudaError_t launch_rows(const RowArgs& a, int sms, cudaStream_t st) {
              : launch_instance<T, MODE, ITEMS, true, THREADS>(a, block, sms, st))
     if (items == 1) return PATCH_ROWS(1, 512);
     if (items == 4) return PATCH_ROWS(4, 512);
+    // (off the boundaries, rows of that length took four groups)
     if constexpr (sizeof(T) == 2)
-        if (block.x > 512) return PATCH_ROWS(2, 1024);
+        if (block.x > 512) return launch_instance<T, MODE, 2, false, 1024>(a, block, sms, st);
     return PATCH_ROWS(2, 512);
 #undef PATCH_ROWS
 }
