@@ -968,22 +968,24 @@ patch_status run_group(patch_group g, const void* const* X, int64_t M, void* con
 }
 
 // How the split-K kernel cuts a call: its form, mb tiles of n_tok tokens (equal
-// ones, a multiple of 16), P parts of K.
+// ones, a multiple of 16), P parts of K, and the rounds in which the GPU holds them.
 struct Q8Split {
-    int config, mb, n_tok, P;
-    int64_t units;
-    double us;  // estimate
+    int config, mb, n_tok, P, kb_max;
+    int64_t units, waves;
+    double us;  // estimate that ranks the forms and parts
 };
 
-// The form with units of bn tokens and the parts of K, at least a slab each, of the
-// least estimate in us. It was fitted to every form and every P for calls of 512 to
-// 13824 rows, 2048 to 11008 columns and 1 to 512 tokens: the choice is within 1 % of
-// the best on average, 13 % at worst, and the estimate of calls of 65 tokens or more
-// within 17 %. A call takes 2 us. Slabs follow one another in a CTA at 0.14 us with
-// six stages or more, at 0.216 with fewer (two CTAs then share an SM's bandwidth); a
-// wave of CTAs costs 1.5 and 2.1 us more (95 % of the slots fill where clusters have
-// to stay within a GPC), and every CTA takes 10 ns, and 0.12 ns a token for its sums,
-// of the whole GPU.
+// The form with units of bn tokens and the parts of K, at least a slab each (the
+// member with the fewest slabs limits P), of the least estimate in us. It was fitted
+// to every form and every P for calls of 512 to 13824 rows, 2048 to 11008 columns and
+// 1 to 512 tokens with 70 % of the tiles 2:4. Measured again at 0, 50 and 100 %, six
+// weights of 512 x 2048 to 13824 x 5120 and 1 to 2048 tokens: the choice takes 2.4 %
+// longer than the best of all forms and parts on average, 19 % at worst (2048 x 2048),
+// alike at all three. A call takes 2 us. Slabs follow one another in a CTA at 0.14 us
+// with six stages or more, at 0.216 with fewer (two CTAs then share an SM's
+// bandwidth); a wave of CTAs costs 1.5 and 2.1 us more (95 % of the slots fill where
+// clusters have to stay within a GPC), and every CTA takes 10 ns, and 0.12 ns a token
+// for its sums, of the whole GPU.
 Q8Split q8_split_plan(patch_group g, int bn, int64_t M) {
     Q8Split x;
     const int64_t mb = (M + bn - 1) / bn;
@@ -1001,6 +1003,8 @@ Q8Split q8_split_plan(patch_group g, int bn, int64_t M) {
     x.us = 1e300;
     x.config = 0;
     x.P = 1;
+    x.kb_max = kb_max;
+    x.waves = 1;
     int config = 0;
     for (const Q8SplitConfig& c : kQ8SplitConfigs) {
         const bool deep = c.stages >= 6;
@@ -1014,6 +1018,7 @@ Q8Split q8_split_plan(patch_group g, int bn, int64_t M) {
                 x.us = us;
                 x.config = config;
                 x.P = p;
+                x.waves = (int64_t)waves;
             }
         }
         ++config;
@@ -1021,30 +1026,51 @@ Q8Split q8_split_plan(patch_group g, int bn, int64_t M) {
     return x;
 }
 
+// Whether CTA pairs with two strips per CTA take a call of more than 64 tokens faster
+// than the split-K kernel does. The two estimates in us were fitted together to both
+// kernels' times for 14 weights of 512 x 2048 to 14336 x 4096 with 0, 50, 70, 90 and
+// 100 % of the tiles 2:4 and 65 to 4096 tokens, calls of nearly equal times weighted
+// most: of 500 choices one costs more than 2 % (9 %).
+// A dense slab takes the split-K kernel 1.23 times a 2:4 one. The wide kernel's two
+// strip pairs move together, so a stage is a fast one where both of their slabs are
+// 2:4; its matrix time goes with the tokens of a tile.
+// Measured, split-K and wide, 50 % 2:4: 2048 x 2048 x 2048 (tokens, rows, columns) 9.9
+// and 15.5 us, 448 x 8192 x 2048 (70 %) 9.4 and 14.6, 256 x 11008 x 4096 15.8 and 18.5,
+// 512 28.7 and 21.4, 768 (two rounds) 31.1 and 34.5, 2048 76 and 58; all 2:4: 768 x
+// 11008 x 4096 29.4 and 26.8, 768 x 4096 x 11008 32.1 and 28.1.
+bool q8_prefers_wide(patch_group g, int64_t M) {
+    int64_t units = 0, work = 0, slabs = 0, sparse = 0, pair_sparse = 0;
+    const int64_t mb = (M + kQ8WideBN - 1) / kQ8WideBN;
+    for (int l = 0; l < g->n; ++l) {
+        const Plan& p = g->h[l]->plan;
+        const int64_t u = (p.S + 3) / 4 * mb;
+        units += u;
+        work += u * p.KB;
+        slabs += (int64_t)p.S * p.KB;
+        sparse += p.sparse;
+        pair_sparse += p.pair_sparse;
+    }
+    const double s = (double)sparse / (double)slabs, ps = (double)pair_sparse / (double)slabs;
+    const double rounds = (double)((units + g->dev.q8_wide_clusters - 1) / g->dev.q8_wide_clusters);
+    const double tile = 32.0 * (double)(((M + 31) / 32 + mb - 1) / mb) / kQ8WideBN;
+    const double wide = 4.8 + rounds * (2.7 + (double)work / (double)units * (0.278 * tile + 0.2 * (1 - ps * ps)));
+    const Q8Split x = q8_split_plan(g, kGemmBN, M);
+    const double slab = (kQ8SplitConfigs[x.config].stages >= 6 ? 0.175 : 0.325) * (s + 1.23 * (1 - s));
+    const double split =
+        0.9 + (double)x.waves * (2.6 + slab * ((x.kb_max + x.P - 1) / x.P)) + 0.0039 * (double)(x.units * x.P);
+    return wide < split;
+}
+
 // The kernel an 8-bit call runs: the split-K kernel with 16- or 64-token units
 // (GEMV, M <= 64) or with 128-token units (GEMM_SINGLE, any M), or CTA pairs
-// with two strips per CTA (GEMM_WIDE, any M). AUTO and GEMM take GEMM_WIDE where
-// its estimate is the lower one: 8 us a call, 0.34 us a slab in every round of
-// quads and 4 us between two rounds. Measured, split-K and wide: 256 x 11008 x
-// 4096 15.4 and 17.7 us, 512 tokens 28.1 and 20.4, 768 (two rounds) 30.5 and 32.8,
-// 2048 76 and 48; 2048 x 4096 x 4096 29.7 and 33.1, 300 x 13824 x 5120 30.7 and 20.5,
-// 2048 x 512 x 2048 5.7 and 13.4.
+// with two strips per CTA (GEMM_WIDE, any M). AUTO and GEMM take the faster one of
+// the last two.
 patch_status resolve_path_q8(patch_group g, int path, int64_t M, int* out) {
     if (M > (int64_t)INT32_MAX / 2) return fail(PATCH_ERR_SHAPE, "M too large");
     M = std::max<int64_t>(1, M);  // patch_group_path may ask about a call that does nothing
     if (path == PATCH_PATH_AUTO && M <= kDecodeWideBN) path = PATCH_PATH_GEMV;
-    if (path == PATCH_PATH_AUTO || path == PATCH_PATH_GEMM) {
-        int64_t units = 0, slabs = 0;
-        for (int l = 0; l < g->n; ++l) {
-            const Plan& p = g->h[l]->plan;
-            const int64_t u = (p.S + 3) / 4 * ((M + kQ8WideBN - 1) / kQ8WideBN);
-            units += u;
-            slabs += u * p.KB;
-        }
-        const int64_t rounds = (units + g->dev.q8_wide_clusters - 1) / g->dev.q8_wide_clusters;
-        const double wide = 4.0 + rounds * (4.0 + 0.34 * slabs / std::max<int64_t>(1, units));
-        path = wide < q8_split_plan(g, kGemmBN, M).us ? PATCH_PATH_GEMM_WIDE : PATCH_PATH_GEMM_SINGLE;
-    }
+    if (path == PATCH_PATH_AUTO || path == PATCH_PATH_GEMM)
+        path = q8_prefers_wide(g, M) ? PATCH_PATH_GEMM_WIDE : PATCH_PATH_GEMM_SINGLE;
     if (path != PATCH_PATH_GEMV && path != PATCH_PATH_GEMM_SINGLE && path != PATCH_PATH_GEMM_WIDE)
         return fail(PATCH_ERR_UNSUPPORTED, "path %d has no 8-bit kernel", path);
     if (path == PATCH_PATH_GEMV && M > kDecodeWideBN)
