@@ -1026,6 +1026,11 @@ Q8Split q8_split_plan(patch_group g, int bn, int64_t M) {
     return x;
 }
 
+// Tokens per unit of the split-K kernel.
+int q8_split_tokens(int path, int64_t M) {
+    return path == PATCH_PATH_GEMM_SINGLE ? kGemmBN : M <= kDecodeBN ? kDecodeBN : kDecodeWideBN;
+}
+
 // Whether CTA pairs with two strips per CTA take a call of more than 64 tokens faster
 // than the split-K kernel does. The two estimates in us were fitted together to both
 // kernels' times for 14 weights of 512 x 2048 to 14336 x 4096 with 0, 50, 70, 90 and
@@ -1065,6 +1070,7 @@ bool q8_prefers_wide(patch_group g, int64_t M) {
 // (GEMV, M <= 64) or with 128-token units (GEMM_SINGLE, any M), or CTA pairs
 // with two strips per CTA (GEMM_WIDE, any M). AUTO and GEMM take the faster one of
 // the last two.
+// Refuses what no kernel can run.
 patch_status resolve_path_q8(patch_group g, int path, int64_t M, int* out) {
     if (M > (int64_t)INT32_MAX / 2) return fail(PATCH_ERR_SHAPE, "M too large");
     M = std::max<int64_t>(1, M);  // patch_group_path may ask about a call that does nothing
@@ -1075,6 +1081,13 @@ patch_status resolve_path_q8(patch_group g, int path, int64_t M, int* out) {
         return fail(PATCH_ERR_UNSUPPORTED, "path %d has no 8-bit kernel", path);
     if (path == PATCH_PATH_GEMV && M > kDecodeWideBN)
         return fail(PATCH_ERR_SHAPE, "the decode kernel takes M <= %d (got %lld)", kDecodeWideBN, (long long)M);
+    // units (times parts of K) are counted in 32 bits
+    const bool wide = path == PATCH_PATH_GEMM_WIDE;
+    const int64_t most = INT32_MAX / (wide ? 2 : kQ8MaxParts);
+    int64_t units = 0;
+    if (!wide) units = q8_split_plan(g, q8_split_tokens(path, M), M).units;
+    for (int l = 0; wide && l < g->n; ++l) units += (g->h[l]->plan.S + 3) / 4 * ((M + kQ8WideBN - 1) / kQ8WideBN);
+    if (units > most) return fail(PATCH_ERR_SHAPE, "M=%lld gives more than %lld output tiles", (long long)M, (long long)most);
     *out = path;
     return PATCH_OK;
 }
@@ -1095,10 +1108,7 @@ struct Q8Call {
 
 template <int G>
 patch_status run_q8_split(patch_group g, const Q8Call& c, int path, cudaStream_t st) {
-    const Q8Split plan = q8_split_plan(
-        g, path == PATCH_PATH_GEMM_SINGLE ? kGemmBN : c.M <= kDecodeBN ? kDecodeBN : kDecodeWideBN, c.M);
-    if (plan.units > INT32_MAX / kQ8MaxParts)
-        return fail(PATCH_ERR_SHAPE, "M=%lld gives more than %d output tiles", (long long)c.M, INT32_MAX / kQ8MaxParts);
+    const Q8Split plan = q8_split_plan(g, q8_split_tokens(path, c.M), c.M);
     Q8Maps<G> maps;
     Q8SplitArgs<G> a;
     a.n_tok = plan.n_tok;
@@ -1166,8 +1176,6 @@ patch_status run_q8_wide(patch_group g, const Q8Call& c, cudaStream_t st) {
         m.KB = h->plan.KB;
         m.unit0 = (int)units;
         units += (h->plan.S + 3) / 4 * mb;
-        if (units > INT32_MAX / 2)
-            return fail(PATCH_ERR_SHAPE, "M=%lld gives more than %d output tiles", (long long)c.M, INT32_MAX / 2);
     }
     a.units = (int)units;
     const int clusters = (int)std::min<int64_t>(units, g->dev.q8_wide_clusters);

@@ -46,3 +46,17 @@ def test_the_faster_kernel(hsg, N, K, split, wide, frac):
 def test_the_share_of_2_4_tiles_decides(hsg, N, K, M):
     assert group(hsg, N, K, 0.0).path(M) == hsg.PATH_GEMM_SINGLE
     assert group(hsg, N, K, 1.0).path(M) == hsg.PATH_GEMM_WIDE
+
+
+def test_path_refuses_what_the_product_refuses(hsg):
+    """2^23 tiles of 128 tokens times 32 strips are more than the launch counts."""
+    g = group(hsg, 4096, 128, 0.5)
+    M = 2 ** 30 - 1
+    x, s = torch.empty(1, 128, dtype=torch.int8, device="cuda"), torch.empty(1, device="cuda")
+    with pytest.raises(hsg.PatchError) as product:
+        hsg._check(hsg.library().patch_linear_q8(g.linears[0].handle, x.data_ptr(), 128, s.data_ptr(), M, x.data_ptr(), 4096,
+                                                 hsg.TYPE_BF16, hsg.PATH_GEMM_SINGLE, None))
+    with pytest.raises(hsg.PatchError) as asked:
+        g.path(M, hsg.PATH_GEMM_SINGLE)
+    assert product.value.status == asked.value.status and str(product.value) == str(asked.value)
+    assert g.path(M, hsg.PATH_GEMM_WIDE) == hsg.PATH_GEMM_WIDE and g.path(2 ** 29, hsg.PATH_GEMM_SINGLE) == hsg.PATH_GEMM_SINGLE
