@@ -9,8 +9,8 @@
 // more than 16384 elements, and operands of more than about 8176 that lie at
 // different offsets from their 16-byte boundaries, are read a second time for the
 // codes. All sums are fp32. A row that holds a NaN or an infinity (or whose sum of
-// squares overflows) gets the scale NaN and zero codes, so that a product
-// over it is NaN instead of silently wrong.
+// squares or product with gamma overflows) gets the scale NaN and zero codes, so
+// that a product over it is NaN instead of silently wrong.
 //
 // The kernels are bound by HBM for many rows and by latency for few. A row is
 // spread over as many threads as give each one or two groups of eight
@@ -792,7 +792,7 @@ cudaError_t launch_rows_type(const RowArgs& a, int mode, int sms, cudaStream_t s
                                       : launch_rows<T, kRowSiluMul>(a, sms, st);
 }
 
-// values = code * scale, one product and one rounding per element, in groups
+// values = code * scale, the fp32 product rounded to the output's type, in groups
 // on the output's 16-byte boundaries. A thread takes kDeq groups, a block's row
 // apart: their loads are in flight together.
 constexpr int kDeq = 2;

@@ -437,8 +437,10 @@ patch_status patch_selftest_wait(void* stream);
  * (both quotients are fp32 divisions, rounded once; ties to even; codes in
  * -127..127), and stands for code * scale. Activations
  * have one scale per token, weights one per output channel. A row that holds a
- * NaN or an infinity, or whose norm's sum of squares overflows fp32, gets the
- * scale NaN and zero codes: what is computed from it is NaN.
+ * NaN or an infinity gets the scale NaN and zero codes: what is computed from it is
+ * NaN. So does one whose intermediate fp32 numbers leave the range: a norm's sum of
+ * squares or a product h * gamma that overflows, a sum of squares that vanishes
+ * with eps = 0.
  *
  * Matrices have rows of contiguous elements and a row pitch (ld, in elements,
  * at least the row's length; ignored for one row). Unless a call says more,
@@ -534,13 +536,15 @@ patch_status patch_rmsnorm_q8(const void* x, int64_t ldx, const void* residual, 
                               int64_t ldo, const void* gamma, int type, float eps, int64_t M, int64_t K, int8_t* q,
                               int64_t ldq, float* scale, void* stream);
 
-/* patch_silu_mul_q8 - the codes and scales of gate / (1 + exp(-gate)) * up. gate
- * and up may be the two halves of one matrix. */
+/* patch_silu_mul_q8 - the codes and scales of gate / (1 + exp(-gate)) * up in fp32,
+ * zero for gates below -88. The exponential is the fast one: for negative gates it is
+ * off by up to 2 + 1.2 |gate| units of 2^-23. gate and up may be the two halves of
+ * one matrix. */
 patch_status patch_silu_mul_q8(const void* gate, int64_t ldg, const void* up, int64_t ldu, int type, int64_t M,
                                int64_t K, int8_t* q, int64_t ldq, float* scale, void* stream);
 
-/* patch_dequantize_q8 - the values code * scale of the rows of q, rounded once to
- * `type`. */
+/* patch_dequantize_q8 - the values code * scale of the rows of q: the fp32 product,
+ * rounded to `type`. */
 patch_status patch_dequantize_q8(const int8_t* q, int64_t ldq, const float* scale, int64_t M, int64_t K, void* out,
                                  int64_t ldo, int type, void* stream);
 

@@ -14,6 +14,7 @@ import synth
 
 pytestmark = pytest.mark.gpu
 TYPES = [torch.bfloat16, torch.float16, torch.float32]
+EPS = 1e-5
 LEAST = np.float32(2.0 ** -126)
 # rows: aligned, off their boundaries, of one warp, of many groups a thread, read twice
 LENGTHS = [(40, 64), (40, 100), (9, 1000), (300, 2048), (12, 4097), (12, 5120), (200, 8192), (5, 13824), (3, 20000)]
@@ -122,3 +123,34 @@ def test_in_earnest(hsg):
     hsg.patch_quantize_q8(x, q, s)
     y = host(x)
     assert np.array_equal(q.cpu().numpy(), divided(y, steps(y)))
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("M,K", LENGTHS)
+@pytest.mark.parametrize("pad,pad_q", [(0, 0), (3, 0), (0, 5)])
+def test_dequantize(hsg, t, M, K, pad, pad_q):
+    """The fp32 product, rounded to the type."""
+    g = synth.generator("cuda", "values", M, K, pad)
+    q = torch.randint(-127, 128, (M, K + pad_q), generator=g, device="cuda", dtype=torch.int8)[:, :K]
+    s = torch.exp2(torch.randint(-20, 4, (M,), generator=g, device="cuda").float()) * (
+        1 + torch.rand(M, generator=g, device="cuda"))
+    out = torch.empty(M, K + pad, dtype=t, device="cuda")[:, :K]
+    hsg.patch_dequantize_q8(q, s, out)
+    assert torch.equal(out.cpu(), (q.cpu().float() * s.cpu()[:, None]).to(t))
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [64, 100, 4096, 20000])
+def test_norms_that_leave_the_range(hsg, t, K):
+    """An overflowing product with gamma, and squares that vanish without an eps,
+    give NaN; with one, the row is an ordinary one."""
+    x, (q, s) = torch.full((4, K), 0.5, dtype=t, device="cuda"), outputs(4, K)
+    x[0] *= 2.0 ** 60
+    x[1] *= 2.0 ** -100
+    big = torch.full((K,), 2.0 ** 70, dtype=t, device="cuda")
+    hsg.patch_rmsnorm_q8(x, big, EPS, q, s)
+    assert s[0].isnan() and not q[0].any() and s[1:].isfinite().all() and (q[1:] == 127).all()
+    hsg.patch_rmsnorm_q8(x, torch.ones_like(big), 0.0, q, s)
+    assert s[1].isnan() and not q[1].any() and s[2:].isfinite().all() and (q[2:] == 127).all()
+    # the first row's squares are 2^118 each: K of them overflow from K = 1024 on
+    assert s[0].isnan() == (K * 2.0 ** 118 >= 2.0 ** 128) and (q[0] == (0 if K >= 1024 else 127)).all()
