@@ -76,10 +76,11 @@ struct Q8SplitArgs {
 // streams its slabs faster than two shallow ones side by side and joins fewer sums,
 // as long as one CTA per SM is the whole call; with more CTAs than that, one joins
 // and stores while the other streams. Measured at 2:4 tiles 70 %, each at its P of
-// the least estimate, one deep and two shallow: 100 x 4096 x 4096 6.6 and 8.3 us, 100 x
-// 11008 x 4096 10.0 and 11.4, 64 x 4096 x 4096 5.7 and 5.9, 200 x 11008 x 4096 (172
-// units) 18.1 and 14.8. 16 tokens: 6 stages x 2 CTAs 4.4 us at 4096 x 4096, 4 x 3 4.5,
-// 3 x 4 and 12 x 1 4.9; 4096 x 11008 8.4, 8.7, 9.1 and 8.4.
+// the least estimate, one deep and two shallow: 100 x 4096 x 4096 6.8 and 8.4 us, 100 x
+// 11008 x 4096 10.4 and 11.6, 64 x 4096 x 4096 5.8 and 6.0, 200 x 11008 x 4096 (172
+// units) 18.1 and 14.9. 16 tokens, measured before the sums were joined in registers:
+// 6 stages x 2 CTAs 4.4 us at 4096 x 4096, 4 x 3 4.5, 3 x 4 and 12 x 1 4.9; 4096 x
+// 11008 8.4 (7.9 now), 8.7, 9.1 and 8.4.
 struct Q8SplitConfig {
     int bn, stages, ctas;
 };

@@ -79,7 +79,7 @@ __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<f
 // behind the arrival. Nothing has to be visible behind this barrier, so the arrival
 // is a relaxed one, and what keeps it behind the reads is its predicate, which is
 // computed from every word read (zero: an argument that is 0, which the compiler
-// does not know). An arrival with release waits for a fence instead: 4.5 us for 4.3
+// does not know). An arrival with release waits for a fence instead: 4.5 us for 4.0
 // at 16 x 4096 x 4096, 3.3 for 2.9 at 16 x 512 x 2048, 11.9 for 11.3 at 100 x 4096 x 11008.
 template <int P, int ITEMS, class Store>
 __device__ __forceinline__ void join(uint32_t base, int rank, int items, uint32_t zero, Store store) {
@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(kThreads, CTAS)
         // ---------------- producer ----------------
         // Weights first out of L2, which leaves the activations in it, and what the
         // neighbours of this call left. Five layers' weights in turn, with the hint and
-        // without: 100 x 11008 x 4096 10.1 and 11.0 us, 16 tokens 8.3 and 8.8; where the
-        // five fit in L2 (4096 x 4096) it costs 3 %, but a model's weights do not.
+        // without: 100 x 11008 x 4096 9.9 and 11.0 us, 16 tokens 8.0 and 8.6; where the
+        // five fit in L2 (4096 x 4096) it costs 1 %, but a model's weights do not.
         const uint64_t pol_w = policy_evict_first();
         auto load_w = [&](int i, uint32_t d) {
             const int st = i % STAGES;

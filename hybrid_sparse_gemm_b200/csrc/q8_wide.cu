@@ -17,9 +17,12 @@
 // pipe's own pace; all pairs together 1.0 to 1.15 times that. Between two tiles of a
 // pair the accumulators are read for 3300 cycles, a sixth of a tile of 32 slabs,
 // but taking the conversions out of it won 1 % of the time only: 2048 x 11008 x
-// 4096 with 90 % 2:4 tiles takes 48 us at the clock of a short run (its MMAs 31 us at
-// twice the bf16 matrix rate), 8192 x 13824 x 5120 253 us, and in a run of seconds,
-// where the card's power limit holds the clock near 1.4 GHz, 301 us.
+// 4096 with 90 % 2:4 tiles of 128 x 128 takes 48 us at the clock of a short run (its
+// MMAs 32 us at twice the bf16 matrix rate, 84 % of the pairs' slabs being 2:4), 8192 x
+// 13824 x 5120 253 us, and in a run of seconds, where the card's power limit holds the
+// clock near 1.4 GHz, 291 us (270 and 311 with tiles of 128 x 64, whose slabs are 2:4
+// in 71 % of the pairs). fp32 outputs are stored before the accumulator is handed
+// back: 54 us for 49, and 358 for 268.
 //
 // TMEM: accumulators in columns [0, 224) and [256, 480), metadata of strip pair
 // 0 at 224 and of pair 1 at 232. All waits are bounded.

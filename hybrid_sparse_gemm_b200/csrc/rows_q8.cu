@@ -747,9 +747,11 @@ cudaError_t launch_rows(const RowArgs& a, int sms, cudaStream_t st) {
     int items = 0;
     // Four groups a thread halve what a row's reduction costs each element, two
     // leave room for more threads. Measured (bf16, us with four and with two): norm
-    // 8192 x 5120 25.2 and 30.6, with residual 47 and 47.8, silu * up 4096 x 8192 32
-    // and 34, but 2048 x 13824 32.3 and 30.1; off the boundaries 2048 x 13823 36
-    // and 43. fp32 (norm and residual, 4096 x 4096): 41 and 35.
+    // 8192 x 5120 25.9 and 32.7, with residual 47.4 and 47.7, quantise 22.6 and 24.6,
+    // silu * up 4096 x 8192 33.2 and 35.2, but 2048 x 13824 33.3 and 31.7 (norm with
+    // residual 4096 x 12288 59.7 and 66.4: with 1024 threads it spills 48 bytes). Off
+    // the boundaries four only: 2048 x 13823 38 (36, and 43 with two, when a code was
+    // one product). fp32 (norm and residual, 4096 x 4096): 43.9 and 34.8.
     const bool four = sizeof(T) == 2 && threads(4) >= 64 && threads(4) <= (aligned ? 256 : 512);
     if (groups <= 64) {
         // a warp per row, eight rows per block
@@ -779,7 +781,7 @@ cudaError_t launch_rows(const RowArgs& a, int sms, cudaStream_t st) {
     if (items == 4) return PATCH_ROWS(4, 512);
     // (off the boundaries, rows of that length took four groups)
     if constexpr (sizeof(T) == 2)
-        if (block.x > 512) return launch_instance<T, MODE, 2, false, 1024>(a, block, sms, st);
+        if (aligned && block.x > 512) return launch_instance<T, MODE, 2, false, 1024>(a, block, sms, st);
     return PATCH_ROWS(2, 512);
 #undef PATCH_ROWS
 }
