@@ -975,6 +975,12 @@ struct Q8Split {
     double us;  // estimate that ranks the forms and parts
 };
 
+// Tokens of a tile: equal tiles of at most bn.
+int q8_split_tile(int bn, int64_t M) {
+    const int64_t mb = (M + bn - 1) / bn;
+    return (int)(((M + mb - 1) / mb + 15) & ~(int64_t)15);
+}
+
 // The form with units of bn tokens and the parts of K, at least a slab each (the
 // member with the fewest slabs limits P), of the least estimate in us. It was fitted
 // to every form and every P for calls of 512 to 13824 rows, 2048 to 11008 columns and
@@ -988,8 +994,7 @@ struct Q8Split {
 // for its sums, of the whole GPU.
 Q8Split q8_split_plan(patch_group g, int bn, int64_t M) {
     Q8Split x;
-    const int64_t mb = (M + bn - 1) / bn;
-    x.n_tok = (int)(((M + mb - 1) / mb + 15) & ~(int64_t)15);
+    x.n_tok = q8_split_tile(bn, M);
     x.mb = (int)((M + x.n_tok - 1) / x.n_tok);
     x.units = 0;
     int kb_min = INT32_MAX, kb_max = 0;
@@ -1083,10 +1088,13 @@ patch_status resolve_path_q8(patch_group g, int path, int64_t M, int* out) {
         return fail(PATCH_ERR_SHAPE, "the decode kernel takes M <= %d (got %lld)", kDecodeWideBN, (long long)M);
     // units (times parts of K) are counted in 32 bits
     const bool wide = path == PATCH_PATH_GEMM_WIDE;
+    const int tile = wide ? kQ8WideBN : q8_split_tile(q8_split_tokens(path, M), M);
     const int64_t most = INT32_MAX / (wide ? 2 : kQ8MaxParts);
     int64_t units = 0;
-    if (!wide) units = q8_split_plan(g, q8_split_tokens(path, M), M).units;
-    for (int l = 0; wide && l < g->n; ++l) units += (g->h[l]->plan.S + 3) / 4 * ((M + kQ8WideBN - 1) / kQ8WideBN);
+    for (int l = 0; l < g->n; ++l) {
+        const int64_t S = g->h[l]->plan.S;
+        units += (wide ? (S + 3) / 4 : S) * ((M + tile - 1) / tile);
+    }
     if (units > most) return fail(PATCH_ERR_SHAPE, "M=%lld gives more than %lld output tiles", (long long)M, (long long)most);
     *out = path;
     return PATCH_OK;
