@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, CTAS)
         const int q = warp & 3;  // TMEM lane quadrant this warp may access
         const int row = q * 32 + lane;
         constexpr int kLeader = 64;  // first thread of the warpgroup
+        bool dead = false;
         int t = 0;
         for (int it = w_begin; it < w_end; ++it, ++t) {
             const int acc = t % ACCS;
@@ -266,9 +267,16 @@ __global__ void __launch_bounds__(kThreads, CTAS)
             const LinDesc& L = a.lins[l];
             const int P = BN == kDecodeBN ? L.P : L.PW;
             const int s = lu / P, p = lu % P;
-            if (!mbar_wait(&acc_full[acc], (t / ACCS) & 1, abort_flag)) {
+            // A warp that gives up still takes its part in the warpgroup's barriers,
+            // at which the others wait for it.
+            dead = dead || !__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], (t / ACCS) & 1, abort_flag));
+            if (dead) {
                 if (lane == 0) raise();
-                break;
+                if (P > 1) {
+                    epi_bar();
+                    epi_bar();
+                }
+                continue;
             }
             tc_fence_after();
             __nv_bfloat16* yc = a.Y[l] + (size_t)s * kStrip + row;
