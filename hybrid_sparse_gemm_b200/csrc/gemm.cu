@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int l = u >> kUnitShift, lu = u & kUnitMask;
             const int N = a.lins[l].N;
             const int s = lu / a.MB, j = lu % a.MB;
-            if (!mbar_wait(&acc_full[acc], acc_phase, abort_flag)) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], acc_phase, abort_flag))) {
                 if (lane == 0) ab.raise();
                 break;
             }

@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool store = pos < a.lins[l].S;
             const int s = store ? a.lins[l].order[pos] : 0;
             const int acc = t & 1;
-            if (!mbar_wait(&acc_full[acc], (t >> 1) & 1, abort_flag)) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], (t >> 1) & 1, abort_flag))) {
                 if (lane == 0) raise();
                 break;
             }

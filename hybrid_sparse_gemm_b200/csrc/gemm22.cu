@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nt = tile_tokens(a, j);
             const int tok0 = tile_start(a, j);
             const int mrem = a.M - tok0;  // tokens of the tile that exist
-            if (!mbar_wait(&acc_full[h], t & 1, abort_flag)) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[h], t & 1, abort_flag))) {
                 if (lane == 0) raise();
                 break;
             }

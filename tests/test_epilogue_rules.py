@@ -12,6 +12,14 @@ from test_source_rules import SOURCES, _code
 KERNELS = [p for p in SOURCES if re.search(r"acc_full", open(p).read())]
 
 
+def test_epilogue_warps_vote():
+    assert len(KERNELS) >= 6
+    for p in KERNELS:
+        waits = re.findall(r"[^;{}]*\bmbar_wait\(&acc_full[^;{}]*", _code(p))
+        for w in waits:
+            assert "__all_sync(0xffffffffu, mbar_wait(&acc_full" in w, f"{os.path.basename(p)}: {w.strip()}"
+
+
 def test_a_warp_that_gave_up_keeps_the_warpgroups_barriers():
     for p in KERNELS:
         code = _code(p)
