@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the layer runs in the CUDA kernels of
 ``libpatch_hybrid.so`` (the C ABI declared in ``include/patch_hybrid.h``).
 PyTorch supplies device memory and streams. If the library is missing this
-module raises on import; there is no fallback.
+module raises on import, and the 8-bit calls raise without the extension that
+marshals them; there is no fallback.
 
     import hybrid_sparse_gemm_b200 as hsg
     lin = hsg.PackedLinear.pack(W, mask_bits, tile_flags, tile_rows=128, tile_cols=128)
